@@ -23,8 +23,9 @@
  *     launched.  mxs_allocate synchronises the stream in one case only:
  *     budget mode over more than one layer, where the greedy needs the
  *     device-computed group gains on the host.
- *   - Device-side failures (a bounded wait that expired) are recorded in a
- *     per-device status word and returned by mxs_sync.
+ *   - Device-side failures (a bounded wait that expired, an index array's
+ *     entry out of range) are recorded in a per-device status word and
+ *     returned by mxs_sync.
  *   - Calls are thread-safe apart from that shared status word.
  */
 #ifndef MXS_H
@@ -132,7 +133,9 @@ int64_t mxs_launch_count(void);
 
 /* Waits for `stream`, then returns and clears the device status word of the
  * current device: MXS_ERR_TIMEOUT if a bounded device wait expired since the
- * last call, MXS_ERR_CUDA if the stream reported an error, else MXS_OK. */
+ * last call, MXS_ERR_SHAPE if a kernel met an index out of range (the calls
+ * that take index arrays say which), MXS_ERR_CUDA if the stream reported an
+ * error, else MXS_OK. */
 mxs_status mxs_sync(void *stream);
 
 /* Diagnostic: sets, on the current device, how many SM clock cycles a
@@ -339,6 +342,142 @@ typedef struct {
 mxs_status mxs_layer_scores_workspace_bytes(const mxs_stack *m, int64_t T, size_t *bytes);
 mxs_status mxs_layer_scores(const mxs_stack *m, const float *x, int64_t T, int64_t ldx, double *scores,
                             void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving operators around the K/V cache: rotary positions, writing new
+ * tokens into the cache and reading them back, and attention of drafted
+ * tokens over it.  The pages keep the K/V cache in MXINT blocks ([TS §4]
+ * W4A4KV4) and say nothing of how tokens enter or leave it; these are the
+ * calls that a program which serves with such a cache makes.
+ *
+ * mxs_rope_plan_make -- the frequencies of a rotary embedding.  Host only.
+ *   The first `rot` positions of a head are turned in pairs i = 0..rot/2-1,
+ *   pair i by the angle pos * f_i: (i, i + rot/2) in the layout
+ *   MXS_ROPE_HALF, (2i, 2i + 1) in MXS_ROPE_INTERLEAVED.  With
+ *   w_i = theta^(-2i/rot) and `turns` t_i = orig_len * w_i / (2 pi):
+ *     MXS_ROPE_PLAIN   f_i = w_i  (also scaling == NULL);
+ *     MXS_ROPE_LINEAR  f_i = w_i / factor;
+ *     MXS_ROPE_PARTS   f_i = w_i (k + (1 - k) / factor),
+ *                      k = clamp((t_i - low) / (high - low), 0, 1);
+ *     MXS_ROPE_YARN    the same with k = 1 - clamp((i - a) / (b - a), 0, 1),
+ *                      a = max(0, floor(p(high))), b = min(rot - 1,
+ *                      ceil(p(low))), b - a taken as at least 0.001, p(n) =
+ *                      rot ln(orig_len / (2 pi n)) / (2 ln theta); cos and
+ *                      sin times 0.1 ln(factor) + 1.
+ *   A frequency is kept as a fraction of a turn in 64-bit fixed point, so
+ *   the phase of position p is the 64-bit product p * step modulo one turn:
+ *   the angle is off by at most |p| * 2^-65 turns, for any int64 position.
+ *   rot even, 2..256; theta > 1; factor >= 1; 0 < low < high and orig_len
+ *   >= 1 where they are used.  Errors: MXS_ERR_ARG. */
+enum { MXS_ROPE_HALF = 0, MXS_ROPE_INTERLEAVED = 1 };
+enum { MXS_ROPE_PLAIN = 0, MXS_ROPE_LINEAR = 1, MXS_ROPE_PARTS = 2, MXS_ROPE_YARN = 3 };
+#define MXS_ROPE_MAX_PAIRS 128
+typedef struct {
+    int32_t kind;
+    double factor, low, high;
+    int64_t orig_len;
+} mxs_rope_scaling;
+typedef struct {
+    int32_t rot, layout;
+    double gain;                          /* factor of cos and sin            */
+    uint64_t step[MXS_ROPE_MAX_PAIRS];    /* turns per position, times 2^64   */
+} mxs_rope_plan;
+mxs_status mxs_rope_plan_make(int32_t rot, int32_t layout, double theta, const mxs_rope_scaling *scaling,
+                              mxs_rope_plan *out);
+
+/* mxs_rope -- rotary positions of T tokens of `heads` heads of d values:
+ *     y_u = x_u cos a - x_v sin a,   y_v = x_v cos a + x_u sin a
+ *   for the pairs (u, v) of the plan, a = pos[t] * f_i; positions rot..d-1
+ *   are copied.  inverse != 0 turns by -a: the operator's transpose, which
+ *   maps the gradient of y to that of x (gain included).
+ *   x (device): token t, head h at x + t*ldxt + h*ldxh (elements), unit
+ *   stride inside a head, dtype xt; out likewise, dtype ot; out may be x
+ *   with the same strides and type, and must not overlap it otherwise, nor
+ *   itself.  pos (device): T int64, any values.  rot <= d <= 256, d even.
+ *   cos and sin are evaluated in 64 bits, the products and their sum too;
+ *   the result is rounded once to fp32, and from there to bf16 if asked. */
+mxs_status mxs_rope(const void *x, mxs_dtype xt, int64_t T, int64_t heads, int64_t d, int64_t ldxt, int64_t ldxh,
+                    const int64_t *pos, const mxs_rope_plan *plan, int32_t inverse, void *out, mxs_dtype ot,
+                    int64_t ldot, int64_t ldoh, void *stream);
+
+/* A K/V cache: a pool of n_slots token slots of n_kvh heads.  K and V are
+ * quantised tensors of n_slots*n_kvh rows in the same identity layout of one
+ * width, {0, 0, d} (4 bits) or {d, 0, 0} (8 bits); row slot*n_kvh + g is kv
+ * head g of the token in that slot.  d: a multiple of 32, at most 256.
+ * (A 4-bit cache of d = 128 is what mxs_attn_decode reads, tokens in slot
+ * order.) */
+typedef struct {
+    mxs_mxtensor K, V;
+    int64_t n_kvh;
+} mxs_kv_cache;
+
+/* mxs_kv_write -- codes T new tokens into their slots of the cache.
+ *   k, v (device): token t, head g at + t*ld?t + g*ld?h (elements), dtype dt,
+ *   finite values; slot (device): T int64, the token's slot; a negative slot
+ *   skips the token (padding).  With plan != NULL the keys are first turned
+ *   to their positions pos (device, T int64) as mxs_rope does and rounded to
+ *   fp32, not to dt; so the cache holds, bit for bit, what mxs_rope to fp32
+ *   followed by mxs_quantize_act gives.  Values are coded as they are.
+ *   Two tokens of one call must not share a slot: the slot then holds a
+ *   mixture of them.  Rows of other slots are not touched.
+ *   A slot >= n_slots is skipped and recorded as MXS_ERR_SHAPE for mxs_sync. */
+mxs_status mxs_kv_write(const void *k, int64_t ldkt, int64_t ldkh, const void *v, int64_t ldvt, int64_t ldvh,
+                        mxs_dtype dt, int64_t T, const int64_t *slot, const int64_t *pos, const mxs_rope_plan *plan,
+                        const mxs_kv_cache *cache, void *stream);
+
+/* mxs_kv_read -- the values that T slots of the cache stand for, exactly
+ * (code * 2^(e - bits + 2), rounded to `ot`: bf16 holds it exactly unless it
+ * leaves that type's range).  k, v (device): where token t, head g goes;
+ * either may be NULL.  A negative slot leaves the token's rows as they are;
+ * a slot >= n_slots does too and is recorded as MXS_ERR_SHAPE for mxs_sync.
+ * A slot may come more than once. */
+mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const int64_t *slot, void *k, int64_t ldkt, int64_t ldkh,
+                       void *v, int64_t ldvt, int64_t ldvh, mxs_dtype ot, void *stream);
+
+/* mxs_attn_tree -- attention of drafted tokens over the paged cache.
+ *   A batch of B sequences.  Sequence b has length[b] tokens in the cache and
+ *   n_b = q_start[b+1] - q_start[b] drafted tokens after them, whose keys
+ *   and values are in the cache too (mxs_kv_write them first): drafted token
+ *   i is the sequence's token length[b] + i.  Token p of sequence b is in
+ *   slot pages[b*ldp + p / page_size] * page_size + p % page_size.
+ *   Row r = q_start[b] + i of q is drafted token i.  It sees all length[b]
+ *   tokens of the context and drafted token j where bit j % 32 of
+ *   mask[r*ldm + j / 32] is set; with mask == NULL it sees j <= i (a chain:
+ *   a chunk of a prompt, or with n_b = 1 one decode step).
+ *     s = sm_scale * q[r][h] . K[p][g],  g = h / (n_qh / n_kvh)
+ *     out[r][h] = sum_p softmax(s)_p V[p][g],  lse[r][h] = ln sum_p e^s
+ *   over the tokens it sees.  A row that sees none gives zeros, and -inf in
+ *   lse.  Rows of q before q_start[0] or from q_start[B] on: their out and
+ *   lse stay as they are.
+ *   q (device): rows x n_qh x d bf16, token and head strides ldqt, ldqh;
+ *   out likewise, dtype ot; lse (device, or NULL): rows x n_qh fp32, dense.
+ *   q 16-byte aligned with strides that are multiples of 8 elements.
+ *   d = 64 or 128; n_qh a multiple of n_kvh.
+ *   batch (host struct; device arrays q_start: B + 1, length: B, pages: B
+ *   rows of pitch ldp, mask: rows of pitch ldm 32-bit words).  max_q >= the
+ *   largest n_b and max_len >= the largest length[b] + n_b set the launch;
+ *   ldp * page_size >= max_len, ldm * 32 >= max_q.  A sequence that breaks
+ *   them (or whose rows leave q, or with a negative length or count) is left
+ *   out, a page outside the pool reads as tokens that no row sees; both are
+ *   recorded as MXS_ERR_SHAPE for mxs_sync.
+ *   ws (device, 256-byte aligned): mxs_attn_tree_workspace_bytes, the
+ *   splits' partial results; calls that may overlap need one each.
+ * Decoded cache values are exact (scale bytes above 249, values of 2^122 and
+ * more, read as 249); scores and sums are fp32.  The weights enter the
+ * product with V in 8 significant bits for a bf16 out, in 16 for fp32. */
+typedef struct {
+    int64_t B, rows, max_q, max_len;
+    const int32_t *q_start, *length;
+    const int32_t *pages;
+    int64_t ldp, page_size;
+    const uint32_t *mask;
+    int64_t ldm;
+} mxs_tree_batch;
+mxs_status mxs_attn_tree_workspace_bytes(const mxs_kv_cache *cache, const mxs_tree_batch *batch, int64_t n_qh,
+                                         size_t *bytes);
+mxs_status mxs_attn_tree(const void *q, int64_t n_qh, int64_t ldqt, int64_t ldqh, const mxs_kv_cache *cache,
+                         const mxs_tree_batch *batch, float sm_scale, void *out, mxs_dtype ot, int64_t ldot,
+                         int64_t ldoh, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

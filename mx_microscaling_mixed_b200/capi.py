@@ -62,6 +62,27 @@ class BudgetC(ctypes.Structure):
                 ("p6_den", ctypes.c_int64), ("fixed8", ctypes.c_int64)]
 
 
+class RopeScalingC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("orig_len", ctypes.c_int64)]
+
+
+class RopePlanC(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("gain", ctypes.c_double),
+                ("step", ctypes.c_uint64 * 128)]
+
+
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("K", MXTensorC), ("V", MXTensorC), ("n_kvh", ctypes.c_int64)]
+
+
+class TreeBatchC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("rows", ctypes.c_int64), ("max_q", ctypes.c_int64),
+                ("max_len", ctypes.c_int64), ("q_start", ctypes.c_void_p), ("length", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("ldp", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("ldm", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -96,13 +117,20 @@ _sig("mxs_layer_scores", [ctypes.POINTER(StackC), _P, _I64, _I64, _P, _P, _SZ, _
 _sig("mxs_attn_decode_workspace_bytes", [_I64, _I64, _I64, _I64, ctypes.POINTER(_SZ)])
 _sig("mxs_attn_decode", [_P, _I64, _I64, ctypes.POINTER(MXTensorC), ctypes.POINTER(MXTensorC), _I64, _I64,
                          ctypes.c_float, _P, _I64, _P, _SZ, _P])
+_sig("mxs_rope_plan_make", [ctypes.c_int32, ctypes.c_int32, ctypes.c_double, _P, _P])
+_sig("mxs_rope", [_P, _ST, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_int32, _P, _ST, _I64, _I64, _P])
+_sig("mxs_kv_write", [_P, _I64, _I64, _P, _I64, _I64, _ST, _I64, _P, _P, _P, _P, _P])
+_sig("mxs_kv_read", [_P, _I64, _P, _P, _I64, _I64, _P, _I64, _I64, _ST, _P])
+_sig("mxs_attn_tree_workspace_bytes", [_P, _P, _I64, _P])
+_sig("mxs_attn_tree", [_P, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _ST, _I64, _I64, _P, _P, _SZ, _P])
 
 EXPORTS = ["mxs_status_str", "mxs_launch_count", "mxs_sync", "mxs_set_wait_limit", "mxs_layout_make", "mxs_mxtensor_bytes",
            "mxs_sensitivity_workspace_bytes", "mxs_sensitivity", "mxs_sensitivity_noalloc",
            "mxs_allocate_workspace_bytes",
            "mxs_allocate", "mxs_quantize_weight", "mxs_quantize_act", "mxs_dequantize",
            "mxs_gemm_workspace_bytes", "mxs_gemm", "mxs_attn_decode_workspace_bytes", "mxs_attn_decode",
-           "mxs_layer_scores_workspace_bytes", "mxs_layer_scores"]
+           "mxs_layer_scores_workspace_bytes", "mxs_layer_scores", "mxs_rope_plan_make", "mxs_rope", "mxs_kv_write",
+           "mxs_kv_read", "mxs_attn_tree_workspace_bytes", "mxs_attn_tree"]
 
 
 def _check(st: int, where: str):
@@ -356,6 +384,278 @@ def mxs_attn_decode(q: torch.Tensor, K: MXTensor, V: MXTensor, T: int, n_kvh: in
                                 float(sm_scale), out.data_ptr(), _rowmajor(out), _aligned_ptr(ws, 256), need,
                                 _stream(stream)), "mxs_attn_decode")
     return out
+
+
+# ------------------------------------------- serving around the K/V cache
+# Every tensor of these calls must be on one device, which need not be the
+# current one; memory the binding allocates is held for the stream it is used
+# on.
+class _On:
+    """The stream handle and the device of a call; makes that device current
+    for its duration where it is not."""
+    __slots__ = ("dev", "stream", "given", "prev")
+
+    def __init__(self, dev: torch.device, stream, others=()):
+        if dev.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}")
+        self.dev, self.given, self.prev = dev, stream, None
+        if stream is None:
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.dev.index:
+            self.prev = cur
+            torch.cuda.set_device(self.dev)
+        return self
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        """Memory for use on the call's stream."""
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=self.dev)):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+
+def _heads(t: torch.Tensor, what: str):
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{what}: expected (tokens, heads, d) with unit stride along d")
+    return t.stride(0), t.stride(1)
+
+
+def _index(t: torch.Tensor, dtype, n: int, what: str) -> int:
+    if t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous {dtype} values")
+    return t.data_ptr()
+
+
+_ROPE_KINDS = {"linear": 1, "parts": 2, "yarn": 3}
+
+
+class RopePlan:
+    """Frequencies of a rotary embedding (mxs_rope_plan_make)."""
+    __slots__ = ("c", "ptr")
+
+    def __init__(self, c: RopePlanC):
+        self.c, self.ptr = c, ctypes.addressof(c)
+
+
+def mxs_rope_plan(rot: int, theta: float = 500000.0, layout: str = "half", scaling: Optional[dict] = None) -> RopePlan:
+    """Plan for the first `rot` positions of a head.  layout: "half" (pairs
+    i, i + rot/2) or "interleaved" (2i, 2i + 1).  scaling: None, or a dict of
+    kind "linear" (factor), "parts" (factor, low, high, orig_len) or "yarn"
+    (factor, orig_len, beta_fast = 32, beta_slow = 1)."""
+    layouts = {"half": 0, "interleaved": 1}
+    if layout not in layouts:
+        raise ValueError(f"unknown rope layout {layout!r}")
+    sc = None
+    if scaling is not None:
+        p = dict(scaling)
+        kind = p.pop("kind", None)
+        if kind not in _ROPE_KINDS:
+            raise ValueError(f"unknown rope scaling {kind!r}")
+        if kind == "yarn":
+            p["low"], p["high"] = p.pop("beta_slow", 1.0), p.pop("beta_fast", 32.0)
+        need = {"factor"} if kind == "linear" else {"factor", "low", "high", "orig_len"}
+        if set(p) != need:
+            raise ValueError(f"rope scaling {kind!r} takes {sorted(need)}, got {sorted(p)}")
+        sc = RopeScalingC(_ROPE_KINDS[kind], float(p["factor"]), float(p.get("low", 0.0)), float(p.get("high", 0.0)),
+                          int(p.get("orig_len", 0)))
+    c = RopePlanC()
+    _check(_lib.mxs_rope_plan_make(int(rot), layouts[layout], float(theta),
+                                   None if sc is None else ctypes.addressof(sc), ctypes.addressof(c)),
+           "mxs_rope_plan_make")
+    return RopePlan(c)
+
+
+def mxs_rope(x: torch.Tensor, pos: torch.Tensor, plan: RopePlan, *, inverse: bool = False,
+             dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x (tokens, heads, d; bf16 or fp32) turned to its positions pos (int64),
+    as `dtype` (x's by default); out may be x.  inverse turns back: the
+    gradient of x from that of the result."""
+    ldxt, ldxh = _heads(x, "x")
+    T, heads, d = x.shape
+    on = _On(x.device, stream, (pos, out))
+    p = _index(pos, torch.int64, T, "pos")
+    if out is None:
+        out = on.empty((T, heads, d), dtype or x.dtype)
+    elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
+        raise ValueError("out: another shape or type than asked for")
+    ldot, ldoh = _heads(out, "out")
+    with on:
+        _check(_lib.mxs_rope(x.data_ptr(), _dt(x), T, heads, d, ldxt, ldxh, p, plan.ptr, bool(inverse),
+                             out.data_ptr(), _dt(out), ldot, ldoh, on.stream), "mxs_rope")
+    return out
+
+
+class KVCache:
+    """A pool of token slots: K and V are MXTensors of n_slots * n_kvh rows
+    (row slot * n_kvh + head) in the same 4- or 8-bit identity layout."""
+
+    def __init__(self, K: MXTensor, V: MXTensor, n_kvh: int):
+        self.K, self.V, self.n_kvh = K, V, int(n_kvh)
+        self.c = KVCacheC(K.c, V.c, int(n_kvh))
+        self.ptr = ctypes.addressof(self.c)
+        self.n_slots, self.d = K.rows // int(n_kvh), K.layout.K
+        dev = [t.device for m in (K, V) for t in (*m.codes, *m.scales) if t is not None]
+        self.device = dev[0] if dev else torch.device("cuda", torch.cuda.current_device())
+        if any(x != self.device for x in dev):
+            raise ValueError("K and V on different devices")
+
+
+def kv_cache_empty(n_slots: int, n_kvh: int, d: int, bits: int = 4, device="cuda") -> KVCache:
+    """A cache of n_slots zeroed token slots; bits 4 or 8."""
+    if bits not in (4, 8):
+        raise ValueError("a K/V cache has 4 or 8 bits")
+    lay = mxs_layout_make(d, (0, 0, d) if bits == 4 else (d, 0, 0))
+    return KVCache(mxtensor_empty(n_slots * n_kvh, lay, device), mxtensor_empty(n_slots * n_kvh, lay, device), n_kvh)
+
+
+def mxs_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slot: torch.Tensor, *,
+                 pos: Optional[torch.Tensor] = None, rope: Optional[RopePlan] = None, stream=None) -> None:
+    """Codes the tokens k, v (tokens, n_kvh, d) into their slots (int64; a
+    negative one skips the token).  With `rope` the keys are turned to pos
+    (int64) first."""
+    ldkt, ldkh = _heads(k, "k")
+    ldvt, ldvh = _heads(v, "v")
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1:] != (cache.n_kvh, cache.d):
+        raise ValueError(f"k, v: expected (tokens, {cache.n_kvh}, {cache.d})")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v of different types")
+    if (rope is None) != (pos is None):
+        raise ValueError("rope and pos come together")
+    on = _On(cache.device, stream, (k, v, slot, pos))
+    s = _index(slot, torch.int64, T, "slot")
+    p = None if pos is None else _index(pos, torch.int64, T, "pos")
+    with on:
+        _check(_lib.mxs_kv_write(k.data_ptr(), ldkt, ldkh, v.data_ptr(), ldvt, ldvh, _dt(k), T, s, p,
+                                 None if rope is None else rope.ptr, cache.ptr, on.stream), "mxs_kv_write")
+
+
+def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """(k, v), each (tokens, n_kvh, d): the values in the given slots (int64).
+    A negative slot leaves its rows of `out` as they are (unspecified where
+    the call makes them)."""
+    T = slot.numel()
+    on = _On(cache.device, stream, (slot,) if out is None else (slot, *out))
+    s = _index(slot, torch.int64, T, "slot")
+    if out is None:
+        out = tuple(on.empty((T, cache.n_kvh, cache.d), dtype) for _ in range(2))
+    k, v = out
+    if k.shape != (T, cache.n_kvh, cache.d) or v.shape != k.shape or k.dtype != v.dtype:
+        raise ValueError(f"out: expected two tensors of ({T}, {cache.n_kvh}, {cache.d}) and one type")
+    with on:
+        _check(_lib.mxs_kv_read(cache.ptr, T, s, k.data_ptr(), *_heads(k, "k"), v.data_ptr(), *_heads(v, "v"), _dt(k),
+                                on.stream), "mxs_kv_read")
+    return k, v
+
+
+class TreeBatch:
+    """Drafted tokens of a batch of sequences over a paged cache."""
+    __slots__ = ("c", "ptr", "rows", "tensors", "device")
+
+    def __init__(self, c: TreeBatchC, tensors):
+        self.c, self.ptr, self.tensors = c, ctypes.addressof(c), tensors
+        self.rows, self.device = int(c.rows), tensors[0].device
+
+
+def tree_batch(q_start: torch.Tensor, length: torch.Tensor, pages: torch.Tensor, page_size: int, *, max_q: int,
+               max_len: int, mask: Optional[torch.Tensor] = None) -> TreeBatch:
+    """q_start (B + 1) and length (B) int32, pages (B, per sequence) int32;
+    mask: (rows, words) int32, bit j % 32 of word j / 32 set where the row
+    sees drafted token j, or None for a chain.  max_q and max_len bound the
+    drafted tokens and the tokens altogether of any sequence.  The tensors
+    are read by each call, so their contents may change between calls.
+    The batch covers q's rows as mask has them, else any number."""
+    B = length.numel()
+    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != B or (pages.shape[1] > 1 and pages.stride(1) != 1):
+        raise ValueError(f"pages: expected ({B}, pages of a sequence) int32 with unit stride")
+    c = TreeBatchC(B, -1, int(max_q), int(max_len), _index(q_start, torch.int32, B + 1, "q_start"),
+                   _index(length, torch.int32, B, "length"), pages.data_ptr(),
+                   pages.stride(0) if B > 1 else pages.shape[1], int(page_size), None, 0)
+    if mask is not None:
+        if mask.dtype != torch.int32 or mask.dim() != 2 or (mask.shape[1] > 1 and mask.stride(1) != 1):
+            raise ValueError("mask: expected (rows, words) int32 with unit stride")
+        if mask.shape[1] * 32 < max_q:
+            raise MxsError(2, "tree_batch")
+        c.mask, c.ldm, c.rows = mask.data_ptr(), mask.stride(0) if mask.shape[0] > 1 else mask.shape[1], mask.shape[0]
+    if max_len > page_size * pages.shape[1]:
+        raise MxsError(2, "tree_batch")
+    dev = length.device
+    for t in (q_start, pages, mask):
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return TreeBatch(c, (length, q_start, pages, mask))
+
+
+def _tree_rows(q: torch.Tensor, batch: TreeBatch) -> TreeBatchC:
+    c = batch.c
+    if c.mask is not None:
+        if batch.rows != q.shape[0]:
+            raise ValueError(f"q has {q.shape[0]} rows, mask {batch.rows}")
+    elif c.rows != q.shape[0]:
+        c = TreeBatchC.from_buffer_copy(c)
+        c.rows = q.shape[0]
+    return c
+
+
+def mxs_attn_tree_workspace_bytes(q: torch.Tensor, cache: KVCache, batch: TreeBatch) -> int:
+    need = _SZ(0)
+    c = _tree_rows(q, batch)
+    _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, ctypes.addressof(c), q.shape[1], ctypes.addressof(need)),
+           "mxs_attn_tree_workspace_bytes")
+    return need.value
+
+
+def attn_tree_workspace(q: torch.Tensor, cache: KVCache, batch: TreeBatch) -> torch.Tensor:
+    """A workspace for mxs_attn_tree calls of these sizes; calls that may
+    overlap need one each."""
+    return _workspace(mxs_attn_tree_workspace_bytes(q, cache, batch), cache.device)
+
+
+def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: float, *,
+                  dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the drafted tokens q (rows, n_qh, d) bf16 over the cache:
+    (rows, n_qh, d) as `dtype` (bf16 or fp32), and with return_lse the fp32
+    (rows, n_qh) logarithms of the sums.  Rows of no sequence stay as they
+    are in `out` (unspecified where the call makes it)."""
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bf16")
+    ldqt, ldqh = _heads(q, "q")
+    rows, n_qh, d = q.shape
+    if d != cache.d:
+        raise ValueError(f"q has heads of {d}, the cache of {cache.d}")
+    on = _On(cache.device, stream, (q, out, workspace, batch))
+    c = _tree_rows(q, batch)
+    cp = ctypes.addressof(c)
+    need = _SZ(0)
+    _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, cp, n_qh, ctypes.addressof(need)), "mxs_attn_tree")
+    if workspace is None:
+        workspace = on.empty(need.value + 1024, torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need.value + 1023:
+        raise MxsError(9, "mxs_attn_tree")
+    if out is None:
+        out = on.empty((rows, n_qh, d), dtype)
+    elif out.shape != q.shape:
+        raise ValueError("out: another shape than q")
+    lse = on.empty((rows, n_qh), torch.float32) if return_lse else None
+    ldot, ldoh = _heads(out, "out")
+    with on:
+        _check(_lib.mxs_attn_tree(q.data_ptr(), n_qh, ldqt, ldqh, cache.ptr, cp, float(sm_scale), out.data_ptr(),
+                                  _dt(out), ldot, ldoh, None if lse is None else lse.data_ptr(),
+                                  _aligned_ptr(workspace, 256), need.value, on.stream), "mxs_attn_tree")
+    return (out, lse) if return_lse else out
 
 
 # ---------------------------------------------------------- layer scores

@@ -1,0 +1,379 @@
+// mxs_cache.cu -- new tokens into the MXINT K/V cache, and back.
+//
+// Coding as the quantisers do: a block of 32 positions has e = floor(log2
+// max|x|) (E8M0 byte e + 127) and codes clamp(rint(x 2^(m-2-e))).  The keys
+// are first turned to their positions, x_u cos a - x_v sin a, rounded once
+// to fp32.
+#include <algorithm>
+
+#include "mxs_cache.cuh"
+#include "mxs_ptx.cuh"
+#include "mxs_rope.cuh"
+
+namespace mxs {
+namespace {
+
+constexpr int kWriteThreads = 256;
+constexpr int kReadThreads = 256;
+constexpr float kRoundMagic = 12582912.0f;       // 1.5 * 2^23: adding it rounds to an integer, ties to even
+constexpr uint32_t kRoundBits = 0x4B400000u;
+
+struct WriteArgs {
+  CacheView c;
+  const void *src[2];
+  int64_t ldt[2], ldh[2];
+  const int64_t *slot, *pos;
+  int64_t T;
+  int32_t rope, tokens;
+  int *status;
+};
+
+// The block's scale factor 2^(m-2-e) from the magnitude bits of its maximum,
+// as two factors: tiny blocks (below 2^-121) need more than one.
+struct CodeScale {
+  float pre, sc;
+  uint32_t byte;
+};
+template <int M>
+__device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits) {
+  CodeScale r;
+  r.byte = amax_bits >> 23;
+  int k = M - 2 - (r.byte == 0 ? -127 : static_cast<int>(r.byte) - 127);
+  r.pre = 1.f;
+  if (k > 127) {
+    r.pre = 18446744073709551616.0f;             // 2^64, exact
+    k -= 64;
+  }
+  r.sc = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+  return r;
+}
+template <int M>
+__device__ __forceinline__ uint32_t code_of(float x, CodeScale s) {
+  constexpr uint32_t L = (1u << (M - 1)) - 1u;
+  const uint32_t b = __float_as_uint(fmaf(x * s.pre, s.sc, kRoundMagic));
+  return min(max(b, kRoundBits - L), kRoundBits + L) & ((1u << M) - 1u);
+}
+
+}  // namespace
+
+// A CTA takes `tokens` tokens at a time; cos and sin of their positions are
+// evaluated once into shared memory and used by all heads.
+//   VEC: a unit is two vectors of 8 values that are n/2 apart in a run of n
+//   positions (n a multiple of 64): both sides of the pairs in the half
+//   layout.  Four neighbouring lanes hold a block of 32 in each vector, so
+//   the block maximum is two shuffles and the codes go out as words.
+//   Otherwise one warp per block, one lane per position.
+template <bool F32, int M, bool VEC>
+__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, const __grid_constant__ mxs_rope_plan plan) {
+  extern __shared__ double2 turn[];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int half = a.rope ? plan.rot >> 1 : 0;
+  const bool inter = plan.layout == MXS_ROPE_INTERLEAVED;
+  const int d = a.c.d, nh = a.c.n_kvh;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
+       t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * half; i += kWriteThreads) {
+      const int t = i / half, p = i - t * half;
+      turn[i] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], false);
+    }
+    if (threadIdx.x < nt && a.slot[t0 + threadIdx.x] >= a.c.n_slots) record_bad_index(a.status);
+    __syncthreads();
+    if constexpr (VEC) {
+      const int per_head = d / 16, per_token = 2 * nh * per_head;    // K units, then V units
+      const int n_units = nt * per_token;
+      for (int base = threadIdx.x - lane; base < n_units; base += kWriteThreads) {
+        const int i = base + lane;
+        const bool in = i < n_units;
+        const int t = in ? i / per_token : 0, r = in ? i - t * per_token : 0;
+        const int isv = r >= nh * per_head, rr = r - isv * nh * per_head;
+        const int h = rr / per_head, u = rr - h * per_head;
+        // K in the half layout: the turned run, then the rest; else one run
+        const int split = !isv && a.rope && !inter ? plan.rot : 0;
+        const int run0 = u < split / 16 ? 0 : split, n = u < split / 16 ? split : d - split;
+        const int e0 = run0 + 8 * (u - run0 / 16), e1 = e0 + n / 2;
+        const int64_t slot = in ? a.slot[t0 + t] : -1;
+        const bool live = slot >= 0 && slot < a.c.n_slots;
+        float v[8], w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = w[k] = 0.f;
+        if (live) {
+          const int64_t si = (t0 + t) * a.ldt[isv] + h * a.ldh[isv];
+          load8<F32>(a.src[isv], si + e0, v);
+          load8<F32>(a.src[isv], si + e1, w);
+          if (!isv && a.rope) {
+            const double2 *cs = turn + t * half;
+            if (!inter) {
+              if (run0 == 0)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) rope_pair(v[k], w[k], cs[e0 + k]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (e0 / 2 + k < half) rope_pair(v[2 * k], v[2 * k + 1], cs[e0 / 2 + k]);
+                if (e1 / 2 + k < half) rope_pair(w[2 * k], w[2 * k + 1], cs[e1 / 2 + k]);
+              }
+            }
+          }
+        }
+        uint32_t mv = 0, mw = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          mv = max(mv, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+          mw = max(mw, __float_as_uint(w[k]) & 0x7FFFFFFFu);
+        }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+          mw = max(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+        }
+        if (!live) continue;
+        const int64_t row = slot * nh + h;
+        uint8_t *cd = a.c.codes[isv] + row * a.c.code_pitch[isv];
+        uint8_t *sd = a.c.scales[isv] + row * a.c.scale_pitch[isv];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const CodeScale s = code_scale<M>(side ? mw : mv);
+          const float(&x)[8] = side ? w : v;
+          const int e = side ? e1 : e0;
+          if constexpr (M == 4) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c |= code_of<4>(x[k], s) << (4 * k);
+            *reinterpret_cast<uint32_t *>(cd + e / 2) = c;
+          } else {
+            uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              c0 |= code_of<8>(x[k], s) << (8 * k);
+              c1 |= code_of<8>(x[4 + k], s) << (8 * k);
+            }
+            *reinterpret_cast<uint2 *>(cd + e) = make_uint2(c0, c1);
+          }
+          if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
+        }
+      }
+    } else {
+      const int nb = d / kBlock, per_token = 2 * nh * nb;
+      for (int i = threadIdx.x >> 5; i < nt * per_token; i += kWriteThreads / 32) {
+        const int t = i / per_token, r = i - t * per_token;
+        const int isv = r >= nh * nb, rr = r - isv * nh * nb;
+        const int h = rr / nb, b = rr - h * nb, e = b * kBlock + lane;
+        const int64_t slot = a.slot[t0 + t];
+        if (slot < 0 || slot >= a.c.n_slots) continue;              // the whole warp
+        const int64_t si = (t0 + t) * a.ldt[isv] + h * a.ldh[isv];
+        float x = load1<F32>(a.src[isv], si + e);
+        if (!isv && a.rope && e < plan.rot) {
+          const bool second = inter ? e & 1 : e >= half;
+          const int p = inter ? e >> 1 : (second ? e - half : e);
+          const int f = inter ? e ^ 1 : (second ? e - half : e + half);
+          float y = load1<F32>(a.src[isv], si + f);
+          if (second) {
+            rope_pair(y, x, turn[t * half + p]);
+          } else {
+            rope_pair(x, y, turn[t * half + p]);
+          }
+        }
+        const CodeScale s = code_scale<M>(__reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7FFFFFFFu));
+        const uint32_t q = code_of<M>(x, s);
+        const uint32_t q1 = __shfl_down_sync(0xffffffffu, q, 1);
+        const int64_t row = slot * nh + h;
+        uint8_t *cd = a.c.codes[isv] + row * a.c.code_pitch[isv];
+        if (M == 8) cd[e] = static_cast<uint8_t>(q);
+        else if ((lane & 1) == 0) cd[e / 2] = static_cast<uint8_t>(q | (q1 << 4));
+        if (lane == 0) a.c.scales[isv][row * a.c.scale_pitch[isv] + b] = static_cast<uint8_t>(s.byte);
+      }
+    }
+  }
+}
+
+namespace {
+
+struct ReadArgs {
+  CacheView c;
+  void *dst[2];
+  int64_t ldt[2], ldh[2];
+  const int64_t *slot;
+  int64_t T;
+  int32_t first, count;      // which of K (0) and V (1)
+  int *status;
+};
+
+}  // namespace
+
+// One thread per 8 values.
+template <bool FOUT, int M, bool VEC>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(ReadArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int per_head = a.c.d / 8, per_side = per_head * a.c.n_kvh, per_token = per_side * a.count;
+  const int64_t total = a.T * per_token;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kReadThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kReadThreads) {
+    const int64_t t = i / per_token;
+    const int r = static_cast<int>(i - t * per_token);
+    const int side = r / per_side, rr = r - side * per_side, sv = a.first + side;
+    const int h = rr / per_head, e = 8 * (rr - h * per_head);
+    const int64_t slot = a.slot[t];
+    if (slot >= a.c.n_slots) record_bad_index(a.status);
+    if (slot < 0 || slot >= a.c.n_slots) continue;
+    const int64_t row = slot * a.c.n_kvh + h;
+    const uint8_t *cd = a.c.codes[sv] + row * a.c.code_pitch[sv];
+    const float step = pow2f(static_cast<int>(a.c.scales[sv][row * a.c.scale_pitch[sv] + e / kBlock]) - 127 - M + 2);
+    float v[8];
+    if constexpr (M == 4) {
+      const uint32_t c = *reinterpret_cast<const uint32_t *>(cd + e / 2);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = code_to_float(static_cast<int>(c << (28 - 4 * k)) >> 28) * step;
+    } else {
+      const uint2 c = *reinterpret_cast<const uint2 *>(cd + e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = code_to_float(static_cast<int>((k < 4 ? c.x : c.y) << (24 - 8 * (k & 3))) >> 24) * step;
+    }
+    const int64_t o = t * a.ldt[sv] + h * a.ldh[sv] + e;
+    if constexpr (VEC) {
+      store8<FOUT>(a.dst[sv], o, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) store1<FOUT>(a.dst[sv], o + k, v[k]);
+    }
+  }
+}
+
+mxs_status cache_view(const mxs_kv_cache *c, CacheView *v) {
+  if (!c || c->n_kvh < 1) return MXS_ERR_ARG;
+  mxs_status st;
+  if ((st = check_mxtensor(&c->K)) != MXS_OK || (st = check_mxtensor(&c->V)) != MXS_OK) return st;
+  const mxs_mxtensor *t[2] = {&c->K, &c->V};
+  const int64_t d = c->K.lay.K;
+  const int seg = c->K.lay.seg[2].k_real == d ? 2 : 0;
+  if (d < kBlock || d > 256 || d % kBlock || c->n_kvh > 65535) return MXS_ERR_SHAPE;
+  if (c->K.rows != c->V.rows || c->K.rows % c->n_kvh || c->K.rows > (int64_t{1} << 40)) return MXS_ERR_SHAPE;
+  for (int i = 0; i < 2; ++i) {
+    if (t[i]->lay.perm || t[i]->lay.K != d || t[i]->lay.seg[seg].k_real != d) return MXS_ERR_SHAPE;
+    v->codes[i] = t[i]->codes[seg];
+    v->scales[i] = t[i]->scales[seg];
+    v->code_pitch[i] = t[i]->code_pitch[seg];
+    v->scale_pitch[i] = t[i]->scale_pitch[seg];
+  }
+  v->n_slots = c->K.rows / c->n_kvh;
+  v->n_kvh = static_cast<int32_t>(c->n_kvh);
+  v->d = static_cast<int32_t>(d);
+  v->bits = kSegBits[seg];
+  return MXS_OK;
+}
+
+namespace {
+
+template <bool F32, int M>
+void launch_write(const WriteArgs &a, const mxs_rope_plan &plan, bool vec, int grid, size_t smem, cudaStream_t s) {
+  if (vec) launch_pdl(kv_write_kernel<F32, M, true>, dim3(grid), dim3(kWriteThreads), smem, s, a, plan);
+  else launch_pdl(kv_write_kernel<F32, M, false>, dim3(grid), dim3(kWriteThreads), smem, s, a, plan);
+}
+template <bool FOUT, int M>
+void launch_read(const ReadArgs &a, bool vec, int grid, cudaStream_t s) {
+  if (vec) launch_pdl(kv_read_kernel<FOUT, M, true>, dim3(grid), dim3(kReadThreads), 0, s, a);
+  else launch_pdl(kv_read_kernel<FOUT, M, false>, dim3(grid), dim3(kReadThreads), 0, s, a);
+}
+
+}  // namespace
+}  // namespace mxs
+
+using namespace mxs;
+
+extern "C" mxs_status mxs_kv_write(const void *k, int64_t ldkt, int64_t ldkh, const void *v, int64_t ldvt,
+                                   int64_t ldvh, mxs_dtype dt, int64_t T, const int64_t *slot, const int64_t *pos,
+                                   const mxs_rope_plan *plan, const mxs_kv_cache *cache, void *stream) {
+  if (T < 0) return MXS_ERR_ARG;
+  if (!dtype_ok(dt)) return MXS_ERR_DTYPE;
+  WriteArgs a{};
+  mxs_status st = cache_view(cache, &a.c);
+  if (st != MXS_OK) return st;
+  if (plan && (st = check_rope_plan(plan, a.c.d)) != MXS_OK) return st;
+  if (T == 0) return MXS_OK;
+  if (!k || !v || !slot || (plan && !pos)) return MXS_ERR_ARG;
+  if (ldkt < 0 || ldkh < 0 || ldvt < 0 || ldvh < 0) return MXS_ERR_SHAPE;
+  if ((st = check_device()) != MXS_OK) return st;
+  a.src[0] = k;
+  a.src[1] = v;
+  a.ldt[0] = ldkt;
+  a.ldh[0] = ldkh;
+  a.ldt[1] = ldvt;
+  a.ldh[1] = ldvh;
+  a.slot = slot;
+  a.pos = pos;
+  a.T = T;
+  a.rope = plan != nullptr;
+  if (!(a.status = device_status_word())) return MXS_ERR_CUDA;
+  const size_t es = dtype_size(dt);
+  const bool half_pairs = plan && plan->layout == MXS_ROPE_HALF;
+  const bool vec = a.c.d % 64 == 0 && (!half_pairs || plan->rot % 64 == 0) && vec8_ok(k, ldkt, ldkh, es) &&
+                   vec8_ok(v, ldvt, ldvh, es);
+  const mxs_rope_plan none{};
+  const int half = plan ? plan->rot / 2 : 0, sms = device_sms();
+  a.tokens = T >= 2 * sms ? 2 : 1;
+  const int64_t steps = (T + a.tokens - 1) / a.tokens;
+  const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 8));
+  const size_t smem = sizeof(double2) * a.tokens * half;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const mxs_rope_plan &p = plan ? *plan : none;
+  if (a.c.bits == 4) {
+    if (dt == MXS_F32) launch_write<true, 4>(a, p, vec, grid, smem, s);
+    else launch_write<false, 4>(a, p, vec, grid, smem, s);
+  } else {
+    if (dt == MXS_F32) launch_write<true, 8>(a, p, vec, grid, smem, s);
+    else launch_write<false, 8>(a, p, vec, grid, smem, s);
+  }
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+extern "C" mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const int64_t *slot, void *k, int64_t ldkt,
+                                  int64_t ldkh, void *v, int64_t ldvt, int64_t ldvh, mxs_dtype ot, void *stream) {
+  if (T < 0) return MXS_ERR_ARG;
+  if (!dtype_ok(ot)) return MXS_ERR_DTYPE;
+  ReadArgs a{};
+  mxs_status st = cache_view(cache, &a.c);
+  if (st != MXS_OK) return st;
+  if (T == 0) return MXS_OK;
+  if (!slot || (!k && !v)) return MXS_ERR_ARG;
+  a.dst[0] = k;
+  a.dst[1] = v;
+  a.ldt[0] = ldkt;
+  a.ldh[0] = ldkh;
+  a.ldt[1] = ldvt;
+  a.ldh[1] = ldvh;
+  a.slot = slot;
+  a.T = T;
+  a.first = k ? 0 : 1;
+  a.count = (k != nullptr) + (v != nullptr);
+  bool vec = true;
+  for (int i = 0; i < 2; ++i) {
+    if (!a.dst[i]) continue;
+    // the rows of the output must not overlap
+    if (a.ldh[i] < a.c.d || a.ldt[i] < a.c.d ||
+        (a.ldt[i] < static_cast<__int128>(a.ldh[i]) * (a.c.n_kvh - 1) + a.c.d &&
+         a.ldh[i] < static_cast<__int128>(a.ldt[i]) * (T - 1) + a.c.d))
+      return MXS_ERR_SHAPE;
+    vec = vec && vec8_ok(a.dst[i], a.ldt[i], a.ldh[i], dtype_size(ot));
+  }
+  if ((st = check_device()) != MXS_OK) return st;
+  if (!(a.status = device_status_word())) return MXS_ERR_CUDA;
+  const int64_t total = T * a.count * a.c.n_kvh * (a.c.d / 8);
+  const int grid = static_cast<int>(std::min<int64_t>((total + kReadThreads - 1) / kReadThreads,
+                                                      static_cast<int64_t>(device_sms()) * 8));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.c.bits == 4) {
+    if (ot == MXS_F32) launch_read<true, 4>(a, vec, grid, s);
+    else launch_read<false, 4>(a, vec, grid, s);
+  } else {
+    if (ot == MXS_F32) launch_read<true, 8>(a, vec, grid, s);
+    else launch_read<false, 8>(a, vec, grid, s);
+  }
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
