@@ -458,13 +458,13 @@ mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const int64_t *slot
  *   largest n_b and max_len >= the largest length[b] + n_b set the launch;
  *   ldp * page_size >= max_len, ldm * 32 >= max_q.  A sequence that breaks
  *   them (or whose rows leave q, or with a negative length or count) is left
- *   out, a page outside the pool reads as tokens that no row sees; both are
+ *   out, a page outside the pool reads as keys and values of zero; both are
  *   recorded as MXS_ERR_SHAPE for mxs_sync.
  *   ws (device, 256-byte aligned): mxs_attn_tree_workspace_bytes, the
  *   splits' partial results; calls that may overlap need one each.
  * Decoded cache values are exact (scale bytes above 249, values of 2^122 and
  * more, read as 249); scores and sums are fp32.  The weights enter the
- * product with V in 8 significant bits for a bf16 out, in 16 for fp32. */
+ * product with V in 8 significant bits for a bf16 out, in 24 for fp32. */
 typedef struct {
     int64_t B, rows, max_q, max_len;
     const int32_t *q_start, *length;
@@ -474,7 +474,7 @@ typedef struct {
     int64_t ldm;
 } mxs_tree_batch;
 mxs_status mxs_attn_tree_workspace_bytes(const mxs_kv_cache *cache, const mxs_tree_batch *batch, int64_t n_qh,
-                                         size_t *bytes);
+                                         mxs_dtype ot, size_t *bytes);
 mxs_status mxs_attn_tree(const void *q, int64_t n_qh, int64_t ldqt, int64_t ldqh, const mxs_kv_cache *cache,
                          const mxs_tree_batch *batch, float sm_scale, void *out, mxs_dtype ot, int64_t ldot,
                          int64_t ldoh, float *lse, void *ws, size_t ws_bytes, void *stream);

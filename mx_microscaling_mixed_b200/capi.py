@@ -121,7 +121,7 @@ _sig("mxs_rope_plan_make", [ctypes.c_int32, ctypes.c_int32, ctypes.c_double, _P,
 _sig("mxs_rope", [_P, _ST, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_int32, _P, _ST, _I64, _I64, _P])
 _sig("mxs_kv_write", [_P, _I64, _I64, _P, _I64, _I64, _ST, _I64, _P, _P, _P, _P, _P])
 _sig("mxs_kv_read", [_P, _I64, _P, _P, _I64, _I64, _P, _I64, _I64, _ST, _P])
-_sig("mxs_attn_tree_workspace_bytes", [_P, _P, _I64, _P])
+_sig("mxs_attn_tree_workspace_bytes", [_P, _P, _I64, _ST, _P])
 _sig("mxs_attn_tree", [_P, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _ST, _I64, _I64, _P, _P, _SZ, _P])
 
 EXPORTS = ["mxs_status_str", "mxs_launch_count", "mxs_sync", "mxs_set_wait_limit", "mxs_layout_make", "mxs_mxtensor_bytes",
@@ -609,18 +609,21 @@ def _tree_rows(q: torch.Tensor, batch: TreeBatch) -> TreeBatchC:
     return c
 
 
-def mxs_attn_tree_workspace_bytes(q: torch.Tensor, cache: KVCache, batch: TreeBatch) -> int:
+def mxs_attn_tree_workspace_bytes(q: torch.Tensor, cache: KVCache, batch: TreeBatch,
+                                  dtype: torch.dtype = torch.bfloat16) -> int:
     need = _SZ(0)
     c = _tree_rows(q, batch)
-    _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, ctypes.addressof(c), q.shape[1], ctypes.addressof(need)),
-           "mxs_attn_tree_workspace_bytes")
+    _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, ctypes.addressof(c), q.shape[1],
+                                              MXS_F32 if dtype == torch.float32 else MXS_BF16,
+                                              ctypes.addressof(need)), "mxs_attn_tree_workspace_bytes")
     return need.value
 
 
 def attn_tree_workspace(q: torch.Tensor, cache: KVCache, batch: TreeBatch) -> torch.Tensor:
-    """A workspace for mxs_attn_tree calls of these sizes; calls that may
-    overlap need one each."""
-    return _workspace(mxs_attn_tree_workspace_bytes(q, cache, batch), cache.device)
+    """A workspace for mxs_attn_tree calls of these sizes, of either output
+    type; calls that may overlap need one each."""
+    return _workspace(max(mxs_attn_tree_workspace_bytes(q, cache, batch, t) for t in (torch.bfloat16, torch.float32)),
+                      cache.device)
 
 
 def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: float, *,
@@ -639,21 +642,23 @@ def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: f
     on = _On(cache.device, stream, (q, out, workspace, batch))
     c = _tree_rows(q, batch)
     cp = ctypes.addressof(c)
-    need = _SZ(0)
-    _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, cp, n_qh, ctypes.addressof(need)), "mxs_attn_tree")
-    if workspace is None:
-        workspace = on.empty(need.value + 1024, torch.uint8)
-    elif workspace.numel() * workspace.element_size() < need.value + 1023:
-        raise MxsError(9, "mxs_attn_tree")
     if out is None:
         out = on.empty((rows, n_qh, d), dtype)
     elif out.shape != q.shape:
         raise ValueError("out: another shape than q")
+    ot = _dt(out)
+    need = _SZ(0)
+    with on:
+        _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, cp, n_qh, ot, ctypes.addressof(need)), "mxs_attn_tree")
+    if workspace is None:
+        workspace = on.empty(need.value + 1024, torch.uint8)
+    elif workspace.numel() * workspace.element_size() < need.value + 255:
+        raise MxsError(9, "mxs_attn_tree")
     lse = on.empty((rows, n_qh), torch.float32) if return_lse else None
     ldot, ldoh = _heads(out, "out")
     with on:
         _check(_lib.mxs_attn_tree(q.data_ptr(), n_qh, ldqt, ldqh, cache.ptr, cp, float(sm_scale), out.data_ptr(),
-                                  _dt(out), ldot, ldoh, None if lse is None else lse.data_ptr(),
+                                  ot, ldot, ldoh, None if lse is None else lse.data_ptr(),
                                   _aligned_ptr(workspace, 256), need.value, on.stream), "mxs_attn_tree")
     return (out, lse) if return_lse else out
 

@@ -101,6 +101,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+// Shared-memory writes of this thread become visible to the tensor core's
+// and the copy engine's reads.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, K-major, 128-byte swizzle: 8-row groups
@@ -110,6 +125,16 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
+}
+// An operand stored along M (or N): W 16-bit elements of M in a row of 2 W
+// bytes (the swizzle's width: 128, 64 or 32), rows of consecutive k, 8-row
+// groups next to each other, the next W elements of M `next` bytes further on.
+template <int W>
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t next) {
+  static_assert(W == 64 || W == 32 || W == 16, "swizzle width");
+  constexpr uint64_t mode = W == 64 ? 2 : W == 32 ? 4 : 6;
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(next >> 4) << 16) |
+         (static_cast<uint64_t>(W) << 32) | (static_cast<uint64_t>(1) << 46) | (mode << 61);
 }
 // Descriptor of one 512-byte scale chunk for tcgen05.cp 32x128b: 32 rows of
 // 16 bytes, no swizzle, 8-row core matrices 128 bytes apart.
