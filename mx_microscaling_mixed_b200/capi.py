@@ -392,44 +392,50 @@ def mxs_attn_decode(q: torch.Tensor, K: MXTensor, V: MXTensor, T: int, n_kvh: in
 # on.
 class _On:
     """The stream handle and the device of a call; makes that device current
-    for its duration where it is not."""
-    __slots__ = ("dev", "stream", "given", "prev")
+    for the call where it is not."""
+    __slots__ = ("dev", "index", "stream", "given")
 
     def __init__(self, dev: torch.device, stream, others=()):
+        index = dev.index
         if dev.type != "cuda":
             raise ValueError("expected CUDA tensors")
         for t in others:
             if t is not None and t.device != dev:
                 raise ValueError(f"tensors on {dev} and {t.device}")
-        self.dev, self.given, self.prev = dev, stream, None
+        self.dev, self.index, self.given = dev, index, stream is not None
         if stream is None:
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
+            self.stream = _current_stream(index)
         else:
             self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.dev.index:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
-        return self
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+    def call(self, f, *args) -> int:
+        """f(*args) with the call's device current; its status."""
+        cur = torch._C._cuda_getDevice()
+        if cur == self.index:
+            return f(*args)
+        torch.cuda.set_device(self.index)
+        try:
+            return f(*args)
+        finally:
+            torch.cuda.set_device(cur)
 
     def empty(self, shape, dtype) -> torch.Tensor:
         """Memory for use on the call's stream."""
-        if self.given is None:
+        if not self.given:
             return torch.empty(shape, dtype=dtype, device=self.dev)
         with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=self.dev)):
             return torch.empty(shape, dtype=dtype, device=self.dev)
 
 
+# the current stream's handle by device index, without the object around it
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _heads(t: torch.Tensor, what: str):
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+    s = t.stride()
+    if len(s) != 3 or (s[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{what}: expected (tokens, heads, d) with unit stride along d")
-    return t.stride(0), t.stride(1)
+    return s[0], s[1]
 
 
 def _index(t: torch.Tensor, dtype, n: int, what: str) -> int:
@@ -491,9 +497,8 @@ def mxs_rope(x: torch.Tensor, pos: torch.Tensor, plan: RopePlan, *, inverse: boo
     elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
         raise ValueError("out: another shape or type than asked for")
     ldot, ldoh = _heads(out, "out")
-    with on:
-        _check(_lib.mxs_rope(x.data_ptr(), _dt(x), T, heads, d, ldxt, ldxh, p, plan.ptr, bool(inverse),
-                             out.data_ptr(), _dt(out), ldot, ldoh, on.stream), "mxs_rope")
+    _check(on.call(_lib.mxs_rope, x.data_ptr(), _dt(x), T, heads, d, ldxt, ldxh, p, plan.ptr, bool(inverse),
+                   out.data_ptr(), _dt(out), ldot, ldoh, on.stream), "mxs_rope")
     return out
 
 
@@ -537,9 +542,8 @@ def mxs_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slot: torch.T
     on = _On(cache.device, stream, (k, v, slot, pos))
     s = _index(slot, torch.int64, T, "slot")
     p = None if pos is None else _index(pos, torch.int64, T, "pos")
-    with on:
-        _check(_lib.mxs_kv_write(k.data_ptr(), ldkt, ldkh, v.data_ptr(), ldvt, ldvh, _dt(k), T, s, p,
-                                 None if rope is None else rope.ptr, cache.ptr, on.stream), "mxs_kv_write")
+    _check(on.call(_lib.mxs_kv_write, k.data_ptr(), ldkt, ldkh, v.data_ptr(), ldvt, ldvh, _dt(k), T, s, p,
+                   None if rope is None else rope.ptr, cache.ptr, on.stream), "mxs_kv_write")
 
 
 def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
@@ -550,13 +554,13 @@ def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torc
     on = _On(cache.device, stream, (slot,) if out is None else (slot, *out))
     s = _index(slot, torch.int64, T, "slot")
     if out is None:
-        out = tuple(on.empty((T, cache.n_kvh, cache.d), dtype) for _ in range(2))
+        shape = (T, cache.n_kvh, cache.d)
+        out = on.empty(shape, dtype), on.empty(shape, dtype)
     k, v = out
     if k.shape != (T, cache.n_kvh, cache.d) or v.shape != k.shape or k.dtype != v.dtype:
         raise ValueError(f"out: expected two tensors of ({T}, {cache.n_kvh}, {cache.d}) and one type")
-    with on:
-        _check(_lib.mxs_kv_read(cache.ptr, T, s, k.data_ptr(), *_heads(k, "k"), v.data_ptr(), *_heads(v, "v"), _dt(k),
-                                on.stream), "mxs_kv_read")
+    _check(on.call(_lib.mxs_kv_read, cache.ptr, T, s, k.data_ptr(), *_heads(k, "k"), v.data_ptr(), *_heads(v, "v"),
+                   _dt(k), on.stream), "mxs_kv_read")
     return k, v
 
 
@@ -648,18 +652,16 @@ def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: f
         raise ValueError("out: another shape than q")
     ot = _dt(out)
     need = _SZ(0)
-    with on:
-        _check(_lib.mxs_attn_tree_workspace_bytes(cache.ptr, cp, n_qh, ot, ctypes.addressof(need)), "mxs_attn_tree")
+    _check(on.call(_lib.mxs_attn_tree_workspace_bytes, cache.ptr, cp, n_qh, ot, ctypes.addressof(need)), "mxs_attn_tree")
     if workspace is None:
         workspace = on.empty(need.value + 1024, torch.uint8)
     elif workspace.numel() * workspace.element_size() < need.value + 255:
         raise MxsError(9, "mxs_attn_tree")
     lse = on.empty((rows, n_qh), torch.float32) if return_lse else None
     ldot, ldoh = _heads(out, "out")
-    with on:
-        _check(_lib.mxs_attn_tree(q.data_ptr(), n_qh, ldqt, ldqh, cache.ptr, cp, float(sm_scale), out.data_ptr(),
-                                  ot, ldot, ldoh, None if lse is None else lse.data_ptr(),
-                                  _aligned_ptr(workspace, 256), need.value, on.stream), "mxs_attn_tree")
+    _check(on.call(_lib.mxs_attn_tree, q.data_ptr(), n_qh, ldqt, ldqh, cache.ptr, cp, float(sm_scale), out.data_ptr(),
+                   ot, ldot, ldoh, None if lse is None else lse.data_ptr(), _aligned_ptr(workspace, 256), need.value,
+                   on.stream), "mxs_attn_tree")
     return (out, lse) if return_lse else out
 
 

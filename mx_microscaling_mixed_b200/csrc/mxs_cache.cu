@@ -61,8 +61,10 @@ __device__ __forceinline__ uint32_t code_of(float x, CodeScale s) {
 //   VEC: a unit is two vectors of 8 values that are n/2 apart in a run of n
 //   positions (n a multiple of 64): both sides of the pairs in the half
 //   layout.  Four neighbouring lanes hold a block of 32 in each vector, so
-//   the block maximum is two shuffles and the codes go out as words.
-//   Otherwise one warp per block, one lane per position.
+//   the block maximum is two shuffles and the codes go out as words.  A
+//   thread keeps one unit of a token and goes through the tokens; the table
+//   holds the k-th pairs of neighbouring units side by side, which leaves no
+//   bank conflict.  Otherwise one warp per block, one lane per position.
 template <bool F32, int M, bool VEC>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, const __grid_constant__ mxs_rope_plan plan) {
   extern __shared__ double2 turn[];
@@ -72,88 +74,87 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, co
   const int half = a.rope ? plan.rot >> 1 : 0;
   const bool inter = plan.layout == MXS_ROPE_INTERLEAVED;
   const int d = a.c.d, nh = a.c.n_kvh;
+  const int group = !VEC ? 1 : inter ? 4 : 8, groups = (half + group - 1) / group;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kWriteThreads) {
       const int t = i / half, p = i - t * half;
-      turn[i] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], false);
+      turn[(t * group + p % group) * groups + p / group] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], false);
     }
     if (threadIdx.x < nt && a.slot[t0 + threadIdx.x] >= a.c.n_slots) record_bad_index(a.status);
     __syncthreads();
     if constexpr (VEC) {
-      const int per_head = d / 16, per_token = 2 * nh * per_head;    // K units, then V units
-      const int n_units = nt * per_token;
-      for (int base = threadIdx.x - lane; base < n_units; base += kWriteThreads) {
-        const int i = base + lane;
-        const bool in = i < n_units;
-        const int t = in ? i / per_token : 0, r = in ? i - t * per_token : 0;
+      const int per_head = d / 16, per_token = 2 * nh * per_head;    // K units, then V units; a multiple of 8
+      const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
+      const int sub = threadIdx.x / wide;
+      if (sub >= abreast) continue;
+      const uint32_t four = 0xFu << (lane & ~3);         // the lanes of a block of 32 values
+      for (int r = threadIdx.x - sub * wide; r < per_token; r += wide) {
         const int isv = r >= nh * per_head, rr = r - isv * nh * per_head;
         const int h = rr / per_head, u = rr - h * per_head;
         // K in the half layout: the turned run, then the rest; else one run
         const int split = !isv && a.rope && !inter ? plan.rot : 0;
         const int run0 = u < split / 16 ? 0 : split, n = u < split / 16 ? split : d - split;
         const int e0 = run0 + 8 * (u - run0 / 16), e1 = e0 + n / 2;
-        const int64_t slot = in ? a.slot[t0 + t] : -1;
-        const bool live = slot >= 0 && slot < a.c.n_slots;
-        float v[8], w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = w[k] = 0.f;
-        if (live) {
+        for (int t = sub; t < nt; t += abreast) {
+          const int64_t slot = a.slot[t0 + t];
+          if (slot < 0 || slot >= a.c.n_slots) continue;              // all lanes of the block
+          float v[8], w[8];
           const int64_t si = (t0 + t) * a.ldt[isv] + h * a.ldh[isv];
           load8<F32>(a.src[isv], si + e0, v);
           load8<F32>(a.src[isv], si + e1, w);
           if (!isv && a.rope) {
-            const double2 *cs = turn + t * half;
+            const double2 *cs = turn + t * group * groups;
             if (!inter) {
-              if (run0 == 0)
+              if (run0 == 0) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) rope_pair(v[k], w[k], cs[e0 + k]);
+                for (int k = 0; k < 8; ++k) rope_pair(v[k], w[k], cs[k * groups + e0 / 8]);
+              }
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                if (e0 / 2 + k < half) rope_pair(v[2 * k], v[2 * k + 1], cs[e0 / 2 + k]);
-                if (e1 / 2 + k < half) rope_pair(w[2 * k], w[2 * k + 1], cs[e1 / 2 + k]);
+                if (e0 / 2 + k < half) rope_pair(v[2 * k], v[2 * k + 1], cs[k * groups + e0 / 8]);
+                if (e1 / 2 + k < half) rope_pair(w[2 * k], w[2 * k + 1], cs[k * groups + e1 / 8]);
               }
             }
           }
-        }
-        uint32_t mv = 0, mw = 0;
+          uint32_t mv = 0, mw = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          mv = max(mv, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-          mw = max(mw, __float_as_uint(w[k]) & 0x7FFFFFFFu);
-        }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-          mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-          mw = max(mw, __shfl_xor_sync(0xffffffffu, mw, o));
-        }
-        if (!live) continue;
-        const int64_t row = slot * nh + h;
-        uint8_t *cd = a.c.codes[isv] + row * a.c.code_pitch[isv];
-        uint8_t *sd = a.c.scales[isv] + row * a.c.scale_pitch[isv];
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const CodeScale s = code_scale<M>(side ? mw : mv);
-          const float(&x)[8] = side ? w : v;
-          const int e = side ? e1 : e0;
-          if constexpr (M == 4) {
-            uint32_t c = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) c |= code_of<4>(x[k], s) << (4 * k);
-            *reinterpret_cast<uint32_t *>(cd + e / 2) = c;
-          } else {
-            uint32_t c0 = 0, c1 = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              c0 |= code_of<8>(x[k], s) << (8 * k);
-              c1 |= code_of<8>(x[4 + k], s) << (8 * k);
-            }
-            *reinterpret_cast<uint2 *>(cd + e) = make_uint2(c0, c1);
+          for (int k = 0; k < 8; ++k) {
+            mv = max(mv, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+            mw = max(mw, __float_as_uint(w[k]) & 0x7FFFFFFFu);
           }
-          if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
+#pragma unroll
+          for (int o = 1; o <= 2; o <<= 1) {
+            mv = max(mv, __shfl_xor_sync(four, mv, o));
+            mw = max(mw, __shfl_xor_sync(four, mw, o));
+          }
+          const int64_t row = slot * nh + h;
+          uint8_t *cd = a.c.codes[isv] + row * a.c.code_pitch[isv];
+          uint8_t *sd = a.c.scales[isv] + row * a.c.scale_pitch[isv];
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const CodeScale s = code_scale<M>(side ? mw : mv);
+            const float(&x)[8] = side ? w : v;
+            const int e = side ? e1 : e0;
+            if constexpr (M == 4) {
+              uint32_t c = 0;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) c |= code_of<4>(x[k], s) << (4 * k);
+              *reinterpret_cast<uint32_t *>(cd + e / 2) = c;
+            } else {
+              uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                c0 |= code_of<8>(x[k], s) << (8 * k);
+                c1 |= code_of<8>(x[4 + k], s) << (8 * k);
+              }
+              *reinterpret_cast<uint2 *>(cd + e) = make_uint2(c0, c1);
+            }
+            if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
+          }
         }
       }
     } else {
@@ -199,47 +200,79 @@ struct ReadArgs {
   const int64_t *slot;
   int64_t T;
   int32_t first, count;      // which of K (0) and V (1)
+  int32_t tokens;            // tokens of a CTA step
   int *status;
 };
 
 }  // namespace
 
-// One thread per 8 values.
+// A thread keeps one place of 8 values of a token (side, head, offset) and
+// goes through tokens, four at a time, so that four loads are in flight and
+// the next tokens' slots are on their way; no index is divided in the loop (with one value group per grid-stride step
+// and its 64-bit division, 131072 tokens of 8 heads of 128 took 266 us).
 template <bool FOUT, int M, bool VEC>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(ReadArgs a) {
   pdl_wait();
   pdl_trigger();
   const int per_head = a.c.d / 8, per_side = per_head * a.c.n_kvh, per_token = per_side * a.count;
-  const int64_t total = a.T * per_token;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kReadThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kReadThreads) {
-    const int64_t t = i / per_token;
-    const int r = static_cast<int>(i - t * per_token);
+  const int wide = min(per_token, kReadThreads), abreast = kReadThreads / wide;
+  const int sub = threadIdx.x / wide;
+  if (sub >= abreast) return;
+  const int64_t t_first = static_cast<int64_t>(blockIdx.x) * a.tokens, t_step = static_cast<int64_t>(gridDim.x) * a.tokens;
+  constexpr int B = 4;
+  for (int r = threadIdx.x - sub * wide; r < per_token; r += wide) {
     const int side = r / per_side, rr = r - side * per_side, sv = a.first + side;
     const int h = rr / per_head, e = 8 * (rr - h * per_head);
-    const int64_t slot = a.slot[t];
-    if (slot >= a.c.n_slots) record_bad_index(a.status);
-    if (slot < 0 || slot >= a.c.n_slots) continue;
-    const int64_t row = slot * a.c.n_kvh + h;
-    const uint8_t *cd = a.c.codes[sv] + row * a.c.code_pitch[sv];
-    const float step = pow2f(static_cast<int>(a.c.scales[sv][row * a.c.scale_pitch[sv] + e / kBlock]) - 127 - M + 2);
-    float v[8];
-    if constexpr (M == 4) {
-      const uint32_t c = *reinterpret_cast<const uint32_t *>(cd + e / 2);
+    const uint8_t *cd = a.c.codes[sv] + e * M / 8, *sd = a.c.scales[sv] + e / kBlock;
+    int64_t next[B];
+    auto slots = [&](int64_t t0) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = code_to_float(static_cast<int>(c << (28 - 4 * k)) >> 28) * step;
-    } else {
-      const uint2 c = *reinterpret_cast<const uint2 *>(cd + e);
+      for (int k = 0; k < B; ++k) {
+        const int64_t t = t0 + sub + k * abreast;
+        next[k] = sub + k * abreast < a.tokens && t < a.T ? __ldg(a.slot + t) : -1;
+      }
+    };
+    slots(t_first);
+    for (int64_t t0 = t_first; t0 < a.T; t0 += t_step) {
+      int64_t row[B];
+      uint2 c[B];
+      uint32_t b[B];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        v[k] = code_to_float(static_cast<int>((k < 4 ? c.x : c.y) << (24 - 8 * (k & 3))) >> 24) * step;
-    }
-    const int64_t o = t * a.ldt[sv] + h * a.ldh[sv] + e;
-    if constexpr (VEC) {
-      store8<FOUT>(a.dst[sv], o, v);
-    } else {
+      for (int k = 0; k < B; ++k) {
+        if (next[k] >= a.c.n_slots) record_bad_index(a.status);
+        row[k] = next[k] >= 0 && next[k] < a.c.n_slots ? next[k] * a.c.n_kvh + h : -1;
+      }
+      if (t0 + t_step < a.T) slots(t0 + t_step);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) store1<FOUT>(a.dst[sv], o + k, v[k]);
+      for (int k = 0; k < B; ++k) {
+        c[k] = make_uint2(0, 0);
+        b[k] = 0;
+        if (row[k] < 0) continue;
+        if constexpr (M == 4) c[k].x = *reinterpret_cast<const uint32_t *>(cd + row[k] * a.c.code_pitch[sv]);
+        else c[k] = *reinterpret_cast<const uint2 *>(cd + row[k] * a.c.code_pitch[sv]);
+        b[k] = sd[row[k] * a.c.scale_pitch[sv]];
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (row[k] < 0) continue;
+        const float step = pow2f(static_cast<int>(b[k]) - 127 - M + 2);
+        float v[8];
+        if constexpr (M == 4) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = code_to_float(static_cast<int>(c[k].x << (28 - 4 * i)) >> 28) * step;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = code_to_float(static_cast<int>((i < 4 ? c[k].x : c[k].y) << (24 - 8 * (i & 3))) >> 24) * step;
+        }
+        const int64_t o = (t0 + sub + k * abreast) * a.ldt[sv] + h * a.ldh[sv] + e;
+        if constexpr (VEC) {
+          store8<FOUT>(a.dst[sv], o, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) store1<FOUT>(a.dst[sv], o + i, v[i]);
+        }
+      }
     }
   }
 }
@@ -315,10 +348,13 @@ extern "C" mxs_status mxs_kv_write(const void *k, int64_t ldkt, int64_t ldkh, co
                    vec8_ok(v, ldvt, ldvh, es);
   const mxs_rope_plan none{};
   const int half = plan ? plan->rot / 2 : 0, sms = device_sms();
-  a.tokens = T >= 2 * sms ? 2 : 1;
+  // as many tokens as the threads take at once, twice where that leaves every SM several CTAs
+  const int64_t per_token = 2 * static_cast<int64_t>(a.c.n_kvh) * (a.c.d / 16);
+  const int64_t abreast = std::max<int64_t>(1, std::min<int64_t>(16, kWriteThreads / per_token));
+  a.tokens = static_cast<int32_t>(T >= 8 * abreast * sms ? 2 * abreast : T >= abreast * sms ? abreast : 1);
   const int64_t steps = (T + a.tokens - 1) / a.tokens;
   const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 8));
-  const size_t smem = sizeof(double2) * a.tokens * half;
+  const size_t smem = sizeof(double2) * a.tokens * ((half + 3) / 4 * 4);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const mxs_rope_plan &p = plan ? *plan : none;
   if (a.c.bits == 4) {
@@ -363,9 +399,12 @@ extern "C" mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const in
   }
   if ((st = check_device()) != MXS_OK) return st;
   if (!(a.status = device_status_word())) return MXS_ERR_CUDA;
-  const int64_t total = T * a.count * a.c.n_kvh * (a.c.d / 8);
-  const int grid = static_cast<int>(std::min<int64_t>((total + kReadThreads - 1) / kReadThreads,
-                                                      static_cast<int64_t>(device_sms()) * 8));
+  // four tokens for every thread, fewer while that leaves SMs without work
+  const int sms = device_sms();
+  const int64_t per_token = static_cast<int64_t>(a.count) * a.c.n_kvh * (a.c.d / 8);
+  const int64_t abreast = std::max<int64_t>(1, kReadThreads / per_token);
+  a.tokens = static_cast<int32_t>(abreast * std::max<int64_t>(1, std::min<int64_t>(4, T / (abreast * 2 * sms))));
+  const int grid = static_cast<int>(std::min<int64_t>((T + a.tokens - 1) / a.tokens, static_cast<int64_t>(sms) * 8));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (a.c.bits == 4) {
     if (ot == MXS_F32) launch_read<true, 4>(a, vec, grid, s);

@@ -23,70 +23,89 @@ struct RopeArgs {
 }  // namespace
 
 // A CTA takes `tokens` tokens at a time: it evaluates their cos and sin once
-// into shared memory, then its threads take the tokens' work units, which
-// all heads share.  VEC: a unit is 8 values of a head (in the half layout, 8
-// values of each side of the pairs); otherwise one pair or one copied value.
+// into shared memory, where all heads find them.  A thread keeps one work
+// unit of a token (head and place in it) and goes through the tokens, so the
+// unit's place is worked out once.  VEC: a unit is 8 values of a head (in the
+// half layout, 8 values of each side of the pairs), and the table holds the
+// k-th pairs of neighbouring units side by side: a unit's reads of it meet no
+// bank conflict (stored pair by pair they took 72 us for 8192 tokens of 32
+// heads of 128, bf16, where the 134 MB of x and y need 20).  Otherwise a unit
+// is one pair or one copied value.
 template <bool FIN, bool FOUT, bool VEC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, const __grid_constant__ mxs_rope_plan plan) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ mxs_rope_plan plan) {
   extern __shared__ double2 turn[];
   pdl_wait();
   pdl_trigger();
   const int half = plan.rot >> 1;
   const bool inter = plan.layout == MXS_ROPE_INTERLEAVED;
   const int step = VEC ? 8 : 1;
+  const int group = !VEC ? 1 : inter ? 4 : 8;            // pairs of a unit
   // units of a head: turned ones first, then copied ones
-  const int turned = VEC ? (inter ? (plan.rot + 7) / 8 : half / 8) : half;
+  const int turned = (half + group - 1) / group;
   const int first_copied = VEC && inter ? turned * 8 : plan.rot;
   const int per_head = turned + (a.d - first_copied) / step;
   const int per_token = per_head * a.heads;
+  const int wide = min(per_token, kRopeThreads);
+  const int abreast = kRopeThreads / wide;               // tokens that the CTA's threads take at once
+  const int sub = threadIdx.x / wide;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
       const int t = i / half, p = i - t * half;
-      turn[i] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], a.inverse);
+      turn[(t * group + p % group) * turned + p / group] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], a.inverse);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * per_token; i += kRopeThreads) {
-      const int t = i / per_token, r = i - t * per_token;
+    if (sub >= abreast) continue;
+    for (int r = threadIdx.x - sub * wide; r < per_token; r += wide) {
       const int h = r / per_head, u = r - h * per_head;
-      const int64_t xi = (t0 + t) * a.ldxt + h * a.ldxh, oi = (t0 + t) * a.ldot + h * a.ldoh;
-      const double2 *cs = turn + t * half;
+      const bool turns = u < turned;
       if constexpr (VEC) {
-        if (u >= turned) {
-          const int e = first_copied + (u - turned) * 8;
-          float v[8];
-          load8<FIN>(a.x, xi + e, v);
-          store8<FOUT>(a.out, oi + e, v);
-        } else if (inter) {
-          const int e = u * 8;
-          float v[8];
-          load8<FIN>(a.x, xi + e, v);
+        // all loads of B tokens first, turned and copied units alike
+        constexpr int B = 2;
+        const int e = turns ? u * 8 : first_copied + (u - turned) * 8;
+        const bool two = turns && !inter;
+        for (int t = sub; t < nt; t += B * abreast) {
+          float v[B][8], w[B][8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (e / 2 + k < half) rope_pair(v[2 * k], v[2 * k + 1], cs[e / 2 + k]);
-          store8<FOUT>(a.out, oi + e, v);
-        } else {
-          const int e = u * 8;
-          float v[8], w[8];
-          load8<FIN>(a.x, xi + e, v);
-          load8<FIN>(a.x, xi + e + half, w);
+          for (int b = 0; b < B; ++b) {
+            const int tb = t + b * abreast;
+            const int64_t xi = (t0 + tb) * a.ldxt + h * a.ldxh + e;
+            if (tb < nt) load8<FIN>(a.x, xi, v[b]);
+            if (tb < nt && two) load8<FIN>(a.x, xi + half, w[b]);
+          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) rope_pair(v[k], w[k], cs[e + k]);
-          store8<FOUT>(a.out, oi + e, v);
-          store8<FOUT>(a.out, oi + e + half, w);
+          for (int b = 0; b < B; ++b) {
+            const int tb = t + b * abreast;
+            if (tb >= nt) break;
+            const double2 *cs = turn + tb * group * turned + u;
+            if (two) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) rope_pair(v[b][k], w[b][k], cs[k * turned]);
+            } else if (turns) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (e / 2 + k < half) rope_pair(v[b][2 * k], v[b][2 * k + 1], cs[k * turned]);
+            }
+            const int64_t oi = (t0 + tb) * a.ldot + h * a.ldoh + e;
+            store8<FOUT>(a.out, oi, v[b]);
+            if (two) store8<FOUT>(a.out, oi + half, w[b]);
+          }
         }
       } else {
-        if (u >= turned) {
-          const int e = plan.rot + u - turned;
-          store1<FOUT>(a.out, oi + e, load1<FIN>(a.x, xi + e));
-        } else {
-          const int e = inter ? 2 * u : u, f = inter ? e + 1 : e + half;
-          float v = load1<FIN>(a.x, xi + e), w = load1<FIN>(a.x, xi + f);
-          rope_pair(v, w, cs[u]);
-          store1<FOUT>(a.out, oi + e, v);
-          store1<FOUT>(a.out, oi + f, w);
+        for (int t = sub; t < nt; t += abreast) {
+          const int64_t xi = (t0 + t) * a.ldxt + h * a.ldxh, oi = (t0 + t) * a.ldot + h * a.ldoh;
+          if (!turns) {
+            const int e = plan.rot + u - turned;
+            store1<FOUT>(a.out, oi + e, load1<FIN>(a.x, xi + e));
+          } else {
+            const int e = inter ? 2 * u : u, f = inter ? e + 1 : e + half;
+            float v = load1<FIN>(a.x, xi + e), w = load1<FIN>(a.x, xi + f);
+            rope_pair(v, w, turn[t * turned + u]);
+            store1<FOUT>(a.out, oi + e, v);
+            store1<FOUT>(a.out, oi + f, w);
+          }
         }
       }
     }
@@ -199,10 +218,10 @@ extern "C" mxs_status mxs_rope(const void *x, mxs_dtype xt, int64_t T, int64_t h
   // four tokens a step (one where there are few), so that a step has about
   // one cos/sin evaluation per thread
   a.tokens = T >= 4 * sms ? std::max(1, 2 * kRopeThreads / half / 2) : 1;
-  a.tokens = std::min(a.tokens, 8);
+  a.tokens = std::min(a.tokens, 4);
   const int64_t steps = (T + a.tokens - 1) / a.tokens;
   const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 8));
-  const size_t smem = sizeof(double2) * a.tokens * half;
+  const size_t smem = sizeof(double2) * a.tokens * ((half + 3) / 4 * 4);    // (interleaved units: whole groups of 4 pairs)
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool fi = xt == MXS_F32, fo = ot == MXS_F32;
   if (fi && fo) launch_rope<true, true>(a, *plan, vec, grid, smem, s);

@@ -54,15 +54,6 @@ __device__ __forceinline__ Sequence sequence_of(const TreeArgs &a, int b, bool r
 __device__ __forceinline__ uint32_t page_of(const TreeArgs &a, uint32_t p) {
   return a.page_mul ? __umulhi(p, a.page_mul) >> a.page_shift : p;
 }
-// Slot of token p of sequence b, or -1 where its page is outside the pool.
-__device__ __forceinline__ int64_t slot_of(const TreeArgs &a, int b, int p) {
-  const uint32_t pg = page_of(a, p);
-  const int page = a.pages[b * a.ldp + pg];
-  const int64_t s = static_cast<int64_t>(page) * a.page_size + (p - pg * a.page_size);
-  const bool ok = page >= 0 && s < a.c.n_slots;
-  if (!ok) record_bad_index(a.status);
-  return ok ? s : -1;
-}
 
 }  // namespace
 
@@ -70,31 +61,37 @@ __device__ __forceinline__ int64_t slot_of(const TreeArgs &a, int b, int p) {
 namespace {
 
 constexpr int kTile = 128;                       // tokens of a tile
-constexpr int kDecodeWarps = 4;
+constexpr int kPeriod = 8;                       // tiles
 constexpr int kAtom = kTile * 128;               // 64 bf16 values of each token of a tile
-constexpr float kSlack = 60.f;                   // weights are kept below 2^kSlack
+constexpr float kSlack = 24.f;                   // weights are kept below 2^kSlack
 constexpr long long kTreeWait = 2000000000LL;    // cycles (about 1 s)
 
 // R columns (query rows) per CTA; P bf16 pieces of a weight.
 template <int D, int M, int R, int P>
 struct Shape {
-  static constexpr int kSoftWarps = R > 64 ? 8 : 4;
-  static constexpr int kCols = R > 64 ? 64 : R;          // columns of a softmax warp
-  static constexpr int kThreads = (kSoftWarps + kDecodeWarps + 1) * 32;
+  static constexpr int kCols = R < 32 ? R : 32;          // columns of a softmax warp
+  static constexpr int kSoftWarps = R / kCols * 4;
+  static constexpr int kResident = R > 32 || (R == 32 && P > 1 && D > 64) ? 1 : 2;
+  static constexpr int kDecodeWarps = kResident == 1 ? 8 : 4;    // 8: four for K, four for V
+  static constexpr int kThreads = (kSoftWarps + kDecodeWarps) * 32;
   static constexpr int kN = R * P;                       // columns of the output product
   static constexpr int kKV = kTile * D * 2;
+  static constexpr int kStages = kResident == 1 && R * P < 192 ? 2 : 1;    // of K and of V
   static constexpr int kPWidth = R < 64 ? R : 64;        // columns in a row of a swizzle atom of the weights
   static constexpr int kPAtom = kTile * kPWidth * 2;
   static constexpr int kPBytes = kTile * kN * 2;
-  static constexpr int kPBufs = 2 * kPBytes + 2 * kKV + R * D * 2 <= 112 * 1024 || R > 64 ? 2 : 1;
-  static constexpr int kK = 0, kV = kKV, kP = 2 * kKV, kQ = kP + kPBufs * kPBytes;
-  static constexpr int kStat = kQ + R * D * 2;           // floats: reference, factor, 4 x maximum or sum per column
-  static constexpr int kBar = kStat + 6 * R * 4;
+  static constexpr int kPBufs = 2;
+  static constexpr int kK = 0, kV = kStages * kKV, kP = 2 * kStages * kKV, kQ = kP + kPBufs * kPBytes;
+  static constexpr int kAcc = kQ + R * D * 2;            // fp32 sums of output periods, [column][place]
+  static constexpr int kStat = kAcc + (P > 1 ? R * D * 4 : 0);   // per column: reference, factor, 4 maxima or sums
+  static constexpr int kPlace = kStat + 6 * R * 4;       // per column: where its output goes (64 bits)
+  static constexpr int kBar = kPlace + R * 8;
+  static constexpr int kBars = kBar + (2 * kStages + 8) * 8 + 16;
   // (heads of 64: the output product reads 64 places that nobody uses behind V's, which have to exist)
-  static constexpr int kEnd = kBar + 9 * 8 + 16 > kV + 2 * kAtom ? kBar + 9 * 8 + 16 : kV + 2 * kAtom;
+  static constexpr int kEnd = kBars > kV + kStages * kKV + kAtom ? kBars : kV + kStages * kKV + kAtom;
   static constexpr int kBytes = kEnd + 1024;
   static constexpr int kTmem = 2 * R + kN <= 64 ? 64 : 2 * R + kN <= 128 ? 128 : 2 * R + kN <= 256 ? 256 : 512;
-  static constexpr int kResident = 2 * (kBytes + 1024) <= 228 * 1024 && kTmem <= 256 && kThreads <= 288 ? 2 : 1;
+  static_assert(kResident * (kBytes + 1024) <= 228 * 1024 && kResident * kTmem <= 512, "the CTAs of an SM fit it");
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTile >> 4) << 24);
   static constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(R >> 3) << 17);
   static constexpr uint32_t kIdescO = kIdesc | (3u << 15) | (static_cast<uint32_t>(kN >> 3) << 17);
@@ -232,33 +229,75 @@ __device__ __forceinline__ TileRange tile_range(const TreeArgs &a, const Sequenc
   return r;
 }
 
+// Sum or maximum of v[k] over the lanes, for each of the N columns k at once:
+// every step halves the columns a lane holds.  Lane l is left with column
+// l * N / 32, in v[0].
+template <int N, typename Op>
+__device__ __forceinline__ float over_lanes(float (&v)[N], int lane, Op op) {
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+
+// Which of 32 tokens, from drafted token j0 on (negative: the context), row i
+// of a sequence sees, one bit each.
+__device__ __forceinline__ uint32_t seen_tokens(const TreeArgs &a, const Sequence &sq, int i, int j0) {
+  if (i >= sq.n) return 0;
+  const int limit = a.mask ? sq.n - j0 : i + 1 - j0;     // tokens up to the last that can be seen
+  uint32_t w = 0xFFFFFFFFu;
+  if (a.mask && j0 > -32) {
+    const uint32_t *m = a.mask + (sq.first + i) * a.ldm;
+    if (j0 < 0) {
+      w = (m[0] << -j0) | ((1u << -j0) - 1u);
+    } else {
+      const int k = j0 >> 5, words = (sq.n + 31) >> 5;
+      w = __funnelshift_r(k < words ? m[k] : 0u, k + 1 < words ? m[k + 1] : 0u, j0 & 31);
+    }
+  }
+  return limit >= 32 ? w : limit <= 0 ? 0u : w & ((1u << limit) - 1u);
+}
+
 }  // namespace
 
 // CTA = (sequence, kv head, split of the tokens, row tile).  Tokens are the
 // 128 rows of the matrix instruction, query rows its columns, so that the
-// work follows the number of rows (16 to 128 of them) while a cache tile is
+// work follows the number of rows (16 to 64 of them) while a cache tile is
 // decoded once for all of them:
 //   S^T [token][row] = K Q^T     A = K  (token x d, K-major),  B = Q
 //   O^T [d][row]    += V^T P^T   A = V  (token x d, stored along d), B = P
-// Both accumulate in tensor memory.  Roles: four warps fetch and decode the
-// cache into shared memory, one thread issues the products, four or eight
-// warps turn scores into weights.  A softmax thread owns one token and sums
-// its weights per row over all tiles; the sums meet at the end.
+// Both accumulate in tensor memory.  Four or eight warps fetch and decode the
+// cache into shared memory, the first of K's and of V's issues the products;
+// four or eight turn scores into weights.  A softmax thread owns one token
+// and sums its weights per row over all tiles; the sums meet at the end.
 //   The running maximum of a row is a reference that weights are relative
 // to, common to all tokens: it is set by the first tile and moved only when
-// a score passes it by more than 2^60, which fp32 and bf16 hold with no loss
-// of precision; so a tile usually needs no maximum, only one vote per 16
-// rows that none of its scores is above.
+// a score passes it by more than 24 (weights of 2^24), which fp32 and bf16 hold with no loss
+// of precision; so a tile usually needs no maximum over its tokens, only one
+// vote that none of its scores is above.
+//   The tensor core's fp32 sums are rounded towards zero at every step: an
+// fp32 output is taken out of tensor memory every kPeriod tiles and summed
+// outside it.
 template <int D, int M, int R, int P, bool FOUT>
 __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>::kResident) tree_kernel(TreeArgs a) {
   using S = Shape<D, M, R, P>;
+  constexpr int NS = S::kStages, C = S::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float *ref = reinterpret_cast<float *>(smem + S::kStat), *factor = ref + R, *wstat = factor + R;   // wstat[4][R]
+  int64_t *place = reinterpret_cast<int64_t *>(smem + S::kPlace);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::kBar);
-  uint64_t *k_full = bar, *v_full = bar + 1, *s_done = bar + 2, *p_full = bar + 4, *o_done = bar + 6,
-           *drained = bar + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 9);
+  uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *drained = bar + 6, *k_full = bar + 8, *v_full = k_full + NS;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(v_full + NS);
   volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -279,13 +318,15 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
     return;
   }
   if (threadIdx.x == 0) {
-    ptx::mbar_init(k_full, kDecodeWarps * 32);
-    ptx::mbar_init(v_full, kDecodeWarps * 32);
-    ptx::mbar_init(drained, 1);
+    for (int i = 0; i < NS; ++i) {
+      ptx::mbar_init(k_full + i, 4 * 32);
+      ptx::mbar_init(v_full + i, 4 * 32);
+    }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
       ptx::mbar_init(s_done + i, 1);
+      ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
       ptx::mbar_init(o_done + i, 1);
+      ptx::mbar_init(drained + i, 1);
     }
     ptx::fence_mbar_init();
     *given_up = 0;
@@ -293,7 +334,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
   for (int i = threadIdx.x; i < R; i += S::kThreads) ref[i] = -INFINITY;
   // tensor memory is taken after the wait for earlier kernels and before
   // later ones may start: a CTA that waits for another kernel holds none
-  if (warp == S::kSoftWarps + kDecodeWarps) {
+  if (warp == 0) {
     ptx::tmem_alloc(tmem_slot, S::kTmem);
     ptx::tmem_relinquish();
   }
@@ -305,86 +346,63 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
   const uint32_t tmem_o = tmem + 2 * R;
   const uint32_t sbase = ptx::smem_addr(smem);
 
-  if (warp == S::kSoftWarps + kDecodeWarps) {
-    // ------------------------------------------------------ matrix products
-    if (lane == 0 && nt > 0) {
-      auto scores = [&](int t) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          ptx::mma_bf16(tmem + (t & 1) * R, ptx::desc_sw128(sbase + S::kK + (k / 4) * kAtom + (k % 4) * 32),
-                        ptx::desc_sw128(sbase + S::kQ + (k / 4) * (R * 128) + (k % 4) * 32), S::kIdescS, k > 0);
-        ptx::mma_commit(s_done + (t & 1));
-      };
-      bool ok = wait_phase(k_full, 0, given_up, a.status);
-      ptx::tc_fence_after();
-      if (ok) scores(0);
-      for (int t = 0; ok && t < nt; ++t) {
-        if (t + 1 < nt) {
-          ok = wait_phase(k_full, (t + 1) & 1, given_up, a.status);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          scores(t + 1);
-        }
-        ok = wait_phase(v_full, t & 1, given_up, a.status) && wait_phase(p_full + (t & 1), (t >> 1) & 1, given_up, a.status);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t pb = sbase + S::kP + (S::kPBufs == 2 ? (t & 1) * S::kPBytes : 0);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          ptx::mma_bf16(tmem_o, ptx::desc_mn<64>(sbase + S::kV + k * 2048, kAtom),
-                        ptx::desc_mn<S::kPWidth>(pb + k * 32 * S::kPWidth, S::kPAtom), S::kIdescO, t > 0 || k > 0);
-        ptx::mma_commit(o_done + (t & 1));
-      }
-      if (!ok) {
-        // leave no product in flight: a last commit covers all that were issued
-        ptx::mma_commit(drained);
-        ptx::mbar_wait_cycles(drained, 0, kTreeWait);
-      }
-    }
-    __syncwarp();
-  } else if (warp >= S::kSoftWarps) {
-    // ------------------------------------------------- fetching and decoding
+  if (warp >= S::kSoftWarps) {
+    // ------------------------------------ fetching, decoding, and the products
+    // Jobs are (tile, K or V): with four warps alternately K and V, with
+    // eight one of them per group.  Two jobs are on their way in registers.
+    constexpr bool kBoth = S::kDecodeWarps == 4;
     constexpr int BL = D / kBlock;                   // blocks of a cache row
-    const int w = warp - S::kSoftWarps, q4 = lane >> 3;
-    const int blk = q4 % BL, sub = q4 / BL;
-    constexpr int kRows = 32 * 4 / BL;               // rows per iteration of the four warps
-    constexpr int kIt = kTile / kRows;
-    const int row_in = w * (8 * 4 / BL) + sub * 8 + (lane & 7);
-    // chunk of 16 bytes c of atom A of row r: 8 lanes on 8 rows hit 8 banks groups
+    constexpr int kRows = 32 / BL;                   // rows per iteration of a warp
+    constexpr int kIt = 32 / kRows;
+    const int dw = warp - S::kSoftWarps, w = dw & 3;
+    const int own = dw >> 2;                         // (eight warps) 0: K, 1: V
+    const int q4 = lane >> 3, blk = q4 % BL;
+    const int row_in = w * 32 + (q4 / BL) * 8 + (lane & 7);
     const uint32_t base = (blk / 2) * kAtom, chunk0 = (blk & 1) * 4;
+    const int jobs = nt <= 0 ? 0 : kBoth ? 2 * nt : nt;
     uint4 raw[2][kIt][M / 4];
     uint32_t sc[2][kIt];
     int64_t at[kIt];
-    auto locate = [&](int t) {
+    int page[kIt];
+    auto look_up = [&](int t) {                      // the pages of a tile
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
         const int p = (tile0 + t) * kTile + it * kRows + row_in;
-        const int64_t slot = p < range.total ? slot_of(a, b, p) : -1;
-        at[it] = slot < 0 ? -1 : slot * a.c.n_kvh + g;
+        page[it] = t < nt && p < range.total ? a.pages[b * a.ldp + page_of(a, p)] : -1;
       }
     };
-    auto fetch = [&](int sv) {
+    auto locate = [&](int t) {                       // its rows in the pool
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const uint32_t p = (tile0 + t) * kTile + it * kRows + row_in;
+        const int64_t slot = static_cast<int64_t>(page[it]) * a.page_size + (p - page_of(a, p) * a.page_size);
+        const bool ok = page[it] >= 0 && slot < a.c.n_slots;
+        if (!ok && t < nt && static_cast<int>(p) < range.total) record_bad_index(a.status);
+        at[it] = ok ? slot * a.c.n_kvh + g : -1;
+      }
+    };
+    auto fetch = [&](int sv, int s) {
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
         if (at[it] >= 0) {
           const uint8_t *c = a.c.codes[sv] + at[it] * a.c.code_pitch[sv] + blk * (kBlock * M / 8);
 #pragma unroll
-          for (int i = 0; i < M / 4; ++i) raw[sv][it][i] = load_stream(c + 16 * i);
-          sc[sv][it] = __ldg(a.c.scales[sv] + at[it] * a.c.scale_pitch[sv] + blk);
+          for (int i = 0; i < M / 4; ++i) raw[s][it][i] = load_stream(c + 16 * i);
+          sc[s][it] = __ldg(a.c.scales[sv] + at[it] * a.c.scale_pitch[sv] + blk);
         } else {
 #pragma unroll
-          for (int i = 0; i < M / 4; ++i) raw[sv][it][i] = make_uint4(0, 0, 0, 0);
-          sc[sv][it] = 0;
+          for (int i = 0; i < M / 4; ++i) raw[s][it][i] = make_uint4(0, 0, 0, 0);
+          sc[s][it] = 0;
         }
       }
     };
-    auto decode = [&](int sv, uint32_t dst) {
+    auto decode = [&](int s, uint32_t dst) {
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
         const int r = it * kRows + row_in;
         uint8_t *rowp = smem + dst + base + r * 128;
-        const BlockScale<M> bs(sc[sv][it]);
-        const uint32_t *wd = reinterpret_cast<const uint32_t *>(&raw[sv][it][0]);
+        const BlockScale<M> bs(sc[s][it]);
+        const uint32_t *wd = reinterpret_cast<const uint32_t *>(&raw[s][it][0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4 *>(rowp + (((chunk0 + j) ^ (r & 7)) << 4)) =
@@ -392,189 +410,266 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
       }
       ptx::fence_async_shared();
     };
-    if (nt > 0) {
-      locate(0);
-      fetch(0);
-      fetch(1);
-      // q: row c of the tile, 16-byte chunks, zero where there is no such row
-      for (int i = threadIdx.x - S::kSoftWarps * 32; i < R * (D / 8); i += kDecodeWarps * 32) {
-        const int c = i / (D / 8), e = i - c * (D / 8);
-        const int rr = row0 + c, di = rr / a.rep, h = rr - di * a.rep;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (di < sq.n)
-          v = *reinterpret_cast<const uint4 *>(a.q + (sq.first + di) * a.ldqt + (g * a.rep + h) * a.ldqh + e * 8);
-        *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) = reorder8<M>(v);
+    auto scores = [&](int t) {                       // one lane: waits for K(t) and the place of its scores
+      bool ok = wait_phase(k_full + t % NS, (t / NS) & 1, given_up, a.status);
+      if (t >= 2) ok = ok && wait_phase(p_full + (t & 1), ((t - 2) >> 1) & 1, given_up, a.status);
+      if (!ok) return false;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        ptx::mma_bf16(tmem + (t & 1) * R, ptx::desc_sw128(sbase + S::kK + (t % NS) * S::kKV + (k / 4) * kAtom + (k % 4) * 32),
+                      ptx::desc_sw128(sbase + S::kQ + (k / 4) * (R * 128) + (k % 4) * 32), S::kIdescS, k > 0);
+      ptx::mma_commit(s_done + (t & 1));
+      return true;
+    };
+    auto output = [&](int t) {                       // one lane: waits for V(t) and its weights
+      const bool ok = wait_phase(v_full + t % NS, (t / NS) & 1, given_up, a.status) &&
+                      wait_phase(p_full + (t & 1), (t >> 1) & 1, given_up, a.status);
+      if (!ok) return false;
+      ptx::tc_fence_after();
+      const bool fresh = P > 1 ? t % kPeriod == 0 : t == 0;
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        ptx::mma_bf16(tmem_o, ptx::desc_mn<64>(sbase + S::kV + (t % NS) * S::kKV + k * 2048, kAtom),
+                      ptx::desc_mn<S::kPWidth>(sbase + S::kP + t % S::kPBufs * S::kPBytes + k * 32 * S::kPWidth, S::kPAtom),
+                      S::kIdescO, !fresh || k > 0);
+      ptx::mma_commit(o_done + (t & 1));
+      return true;
+    };
+    // what the fetch of job j + 2 needs
+    auto advance = [&](int j) {
+      if (kBoth && (j & 1)) return;                  // V of the same tile
+      const int t = kBoth ? j >> 1 : j;
+      locate(t);
+      look_up(t + 1);
+    };
+    if (jobs > 0) {
+      look_up(0);
+      advance(0);
+      fetch(kBoth ? 0 : own, 0);
+      advance(1);
+      fetch(kBoth ? 1 : own, 1);
+      if (kBoth || own == 0) {
+        // q: row c of the tile, 16-byte chunks, zero where there is no such row
+        for (int i = (dw & 3) * 32 + lane; i < R * (D / 8); i += 128) {
+          const int c = i / (D / 8), e = i - c * (D / 8);
+          const int rr = row0 + c, di = rr / a.rep, h = rr - di * a.rep;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (di < sq.n)
+            v = *reinterpret_cast<const uint4 *>(a.q + (sq.first + di) * a.ldqt + (g * a.rep + h) * a.ldqh + e * 8);
+          *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) = reorder8<M>(v);
+        }
       }
     }
     bool ok = true;
-    for (int t = 0; t < nt; ++t) {
-      const int u = t - 1;
-      if (t > 0) ok = wait_phase(s_done + (u & 1), (u >> 1) & 1, given_up, a.status);
-      if (!ok) break;
-      decode(0, S::kK);
-      ptx::mbar_arrive(k_full);
-      if (t + 1 < nt) {
-        locate(t + 1);
-        fetch(0);
+    auto job = [&](int j, int s) {
+      const int t = kBoth ? j >> 1 : j;
+      const int isv = kBoth ? s : own;
+      const int u = t - NS;                          // the tile whose place this one takes
+      if (u >= 0) ok = wait_phase((isv ? o_done : s_done) + (u & 1), (u >> 1) & 1, given_up, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      decode(s, (isv ? S::kV : S::kK) + (t % NS) * S::kKV);
+      ptx::mbar_arrive((isv ? v_full : k_full) + t % NS);
+      if (j + 2 < jobs) {
+        advance(j + 2);
+        fetch(isv, s);
       }
-      if (t > 0) ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
-      if (!ok) break;
-      decode(1, S::kV);
-      ptx::mbar_arrive(v_full);
-      if (t + 1 < nt) fetch(1);
+      if (w == 0) {
+        if (lane == 0) {
+          if (!isv) {
+            ok = scores(t);
+            if (kBoth && t > 0) ok = ok && output(t - 1);
+          } else if (!kBoth || t == nt - 1) {
+            ok = output(t);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+    };
+    for (int j = 0; j < jobs && ok; j += 2) {
+      job(j, 0);
+      if (j + 1 < jobs && ok) job(j + 1, 1);
     }
+    if (!ok && w == 0 && lane == 0) {
+      // leave no product in flight: a last commit covers all that this thread issued
+      ptx::mma_commit(drained + own);
+      ptx::mbar_wait_cycles(drained + own, 0, kTreeWait);
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
     const int grp = warp >> 2, w4 = warp & 3;
-    const int tok = w4 * 32 + lane, col0 = grp * 64;
+    const int tok = w4 * 32 + lane, col0 = grp * C;
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
     // the swizzle of a row of 128, 64 or 32 bytes
     const int pswz = S::kPWidth == 64 ? tok & 7 : S::kPWidth == 32 ? (tok >> 1) & 3 : (tok >> 2) & 1;
-    float sum[S::kCols];
+    float *acc = reinterpret_cast<float *>(smem + S::kAcc) + col0 * D + tok;
+    float sum[C];
 #pragma unroll
-    for (int k = 0; k < S::kCols; ++k) sum[k] = 0.f;
+    for (int k = 0; k < C; ++k) sum[k] = 0.f;
     bool ok = true;
-    for (int t = 0; t < nt && ok; ++t) {
+    auto load_scores = [&](int t, uint32_t (&s)[C]) {
+#pragma unroll
+      for (int c0 = 0; c0 < C; c0 += 16)
+        ptx::tmem_ld16(tmem + lanes + (t & 1) * R + col0 + c0, *reinterpret_cast<uint32_t(*)[16]>(&s[c0]));
+      ptx::tmem_wait_ld();
+    };
+    for (int t = 0; t < nt; ++t) {
       ok = wait_phase(s_done + (t & 1), (t >> 1) & 1, given_up, a.status);
+      ptx::tc_fence_after();
+      uint32_t see = 0xFFFFFFFFu;
+      if ((tile0 + t + 1) * kTile > range.open) {
+        // lane k: column k's tokens of this warp, then exchanged
+        const int j0 = (tile0 + t) * kTile + w4 * 32 - sq.ctx;
+        const uint32_t mine = seen_tokens(a, sq, (row0 + col0 + lane % C) / a.rep, j0);
+        see = 0;
+#pragma unroll
+        for (int k = 0; k < C; ++k) see |= (__shfl_sync(0xffffffffu, mine, k) >> lane & 1u) << k;
+      }
+      uint32_t s[C];
+      load_scores(t, s);
+      float v[C], top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < C; k += 4) {
+        const float4 r = *reinterpret_cast<const float4 *>(ref + col0 + k);
+        v[k] = fmaf(__uint_as_float(s[k]), a.scale_log2, -r.x);
+        v[k + 1] = fmaf(__uint_as_float(s[k + 1]), a.scale_log2, -r.y);
+        v[k + 2] = fmaf(__uint_as_float(s[k + 2]), a.scale_log2, -r.z);
+        v[k + 3] = fmaf(__uint_as_float(s[k + 3]), a.scale_log2, -r.w);
+      }
+      if (see != 0xFFFFFFFFu) {
+#pragma unroll
+        for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        top = fmaxf(top, v[k]);
+        v[k] = exp2_fast(v[k]);
+      }
+      // (its vote below also carries a wait that ran out: all of the group leave together)
       if (t >= S::kPBufs) {
         const int u = t - S::kPBufs;
-        ok = ok && wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
+        ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status) && ok;
       }
-      ptx::tc_fence_after();
-      const int p = (tile0 + t) * kTile + tok;
-      const bool masked = (tile0 + t + 1) * kTile > range.open;
-      uint8_t *prow = smem + S::kP + (S::kPBufs == 2 ? (t & 1) * S::kPBytes : 0) + tok * (2 * S::kPWidth);
-#pragma unroll
-      for (int c0 = 0; c0 < S::kCols; c0 += 16) {
-        uint32_t s[16];
-        ptx::tmem_ld16(tmem + lanes + (t & 1) * R + col0 + c0, s);
-        uint32_t see = 0xFFFFu;
-        if (masked) {
-          see = 0;
-          if (p < sq.ctx) {
-            see = 0xFFFFu;
-          } else if (p < range.total) {
-            const int j = p - sq.ctx;
-            int i = (row0 + col0 + c0) / a.rep, h = row0 + col0 + c0 - i * a.rep;
-            bool sees = false, fresh = true;
-            for (int k = 0; k < 16; ++k) {
-              if (fresh)
-                sees = i < sq.n && (a.mask ? (a.mask[(sq.first + i) * a.ldm + (j >> 5)] >> (j & 31)) & 1u : j <= i);
-              see |= static_cast<uint32_t>(sees) << k;
-              fresh = ++h == a.rep;
-              if (fresh) {
-                h = 0;
-                ++i;
-              }
-            }
-          }
+      const bool flush = P > 1 && t > 0 && t % kPeriod == 0;
+      if (any_of(grp, top > kSlack || !ok || flush)) {
+        // rare: a reference is overtaken (or not set yet), or an output period ends
+        if (t > 0 && ok) {
+          const int u = t - 1;
+          ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
+          ptx::tc_fence_after();
         }
-        ptx::tmem_wait_ld();
-        float v[16], top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(s[k]), a.scale_log2, -ref[col0 + c0 + k]);
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
+        if (any_of(grp, !ok)) {
+          ok = false;
+          break;
         }
+        load_scores(t, s);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) top = fmaxf(top, v[k]);
-        if (any_of(grp, top > kSlack || !ok)) {
-          // a reference is overtaken (or not set yet): move those of these 16
-          // columns to the larger of themselves and the tile's maximum
-          bool stop = !ok;
-          if (t > 0 && !stop) {
-            const int u = t - 1;
-            stop = !wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
-            ptx::tc_fence_after();
-          }
-          if (any_of(grp, stop)) {
-            ok = false;
-            break;
-          }
-          ptx::tmem_ld16(tmem + lanes + (t & 1) * R + col0 + c0, s);
-          ptx::tmem_wait_ld();
-          float mine = -INFINITY;
+        for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? __uint_as_float(s[k]) * a.scale_log2 : -INFINITY;
+        {
+          float m[C];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            v[k] = (see >> k) & 1u ? __uint_as_float(s[k]) * a.scale_log2 : -INFINITY;
-            float m = v[k];
+          for (int k = 0; k < C; ++k) m[k] = v[k];
+          const float mine = over_lanes(m, lane, [](float p, float q) { return fmaxf(p, q); });
+          if (lane % (32 / C) == 0) wstat[w4 * R + col0 + lane / (32 / C)] = mine;
+        }
+        group_sync(grp);
+        if (tok < C) {
+          // references move only as far as they have to: by nothing, unless passed by 2^kSlack
+          const int c = col0 + tok;
+          const float old = ref[c];
+          float m = fmaxf(fmaxf(wstat[c], wstat[R + c]), fmaxf(wstat[2 * R + c], wstat[3 * R + c]));
+          m = m - old > kSlack || old == -INFINITY ? m : old;
+          factor[c] = m == old ? 1.f : exp2f(old - m);
+          ref[c] = m;
+        }
+        group_sync(grp);
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == k) mine = m;
-          }
-          if (lane < 16) wstat[w4 * R + col0 + c0 + lane] = mine;
-          group_sync(grp);
-          if (w4 == 0 && lane < 16) {
-            const int c = col0 + c0 + lane;
-            const float old = ref[c];
-            const float m = fmaxf(fmaxf(fmaxf(wstat[c], wstat[R + c]), fmaxf(wstat[2 * R + c], wstat[3 * R + c])), old);
-            factor[c] = m == old ? 1.f : exp2f(old - m);
-            ref[c] = m;
-          }
-          group_sync(grp);
-          float f[16];
+        for (int k = 0; k < C; ++k) {
+          sum[k] *= factor[col0 + k];
+          v[k] = (see >> k) & 1u ? exp2_fast(v[k] - ref[col0 + k]) : 0.f;
+        }
+        if (t > 0) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < C; c0 += 16) {
+            float part[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            f[k] = factor[col0 + c0 + k];
-            sum[c0 + k] *= f[k];
-            v[k] = (see >> k) & 1u ? v[k] - ref[col0 + c0 + k] : -INFINITY;
-          }
-          if (t > 0) {
-#pragma unroll
-            for (int q = 0; q < P; ++q) {
+            for (int k = 0; k < 16; ++k) part[k] = 0.f;
+#pragma unroll 1
+            for (int q = P - 1; q >= 0; --q) {
               uint32_t o[16];
               ptx::tmem_ld16(tmem_o + lanes + q * R + col0 + c0, o);
               ptx::tmem_wait_ld();
+              if (flush) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[k]);
-              ptx::tmem_st16(tmem_o + lanes + q * R + col0 + c0, o);
+                for (int k = 0; k < 16; ++k) part[k] += __uint_as_float(o[k]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor[col0 + c0 + k]);
+                ptx::tmem_st16(tmem_o + lanes + q * R + col0 + c0, o);
+              }
             }
-            ptx::tmem_wait_st();
-          }
-        }
+            if (P > 1 && tok < D && (flush || t > kPeriod)) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          v[k] = exp2_fast(v[k]);
-          sum[c0 + k] += v[k];
+              for (int k = 0; k < 16; ++k) {
+                float *z = acc + (c0 + k) * D;
+                *z = ((t > kPeriod ? *z : 0.f) + part[k]) * factor[col0 + c0 + k];
+              }
+            }
+          }
+          ptx::tmem_wait_st();
         }
-        // the weights as P bf16 pieces, each the rounding of what the ones before left
+        group_sync(grp);                             // (factor and wstat may be written again)
+      }
+      // the weights as P bf16 pieces, each the rounding of what the ones before left
+      uint8_t *prow = smem + S::kP + t % S::kPBufs * S::kPBytes + tok * (2 * S::kPWidth);
+#pragma unroll
+      for (int k = 0; k < C; ++k) sum[k] += v[k];
+#pragma unroll
+      for (int c0 = 0; c0 < C; c0 += 8) {
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-          uint32_t o[8];
+          uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            o[k] = pack2(v[2 * k], v[2 * k + 1]);
+          for (int k = 0; k < 4; ++k) {
+            o[k] = pack2(v[c0 + 2 * k], v[c0 + 2 * k + 1]);
             if (q + 1 < P) {
-              v[2 * k] -= __uint_as_float(o[k] << 16);
-              v[2 * k + 1] -= __uint_as_float(o[k] & 0xFFFF0000u);
+              v[c0 + 2 * k] -= __uint_as_float(o[k] << 16);
+              v[c0 + 2 * k + 1] -= __uint_as_float(o[k] & 0xFFFF0000u);
             }
           }
           const int cc = q * R + col0 + c0;
-          uint8_t *pr = prow + (cc / S::kPWidth) * S::kPAtom;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<uint4 *>(pr + ((((cc % S::kPWidth) / 8 + k) ^ pswz) << 4)) =
-                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          *reinterpret_cast<uint4 *>(prow + (cc / S::kPWidth) * S::kPAtom + (((cc % S::kPWidth) / 8 ^ pswz) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      if (!ok) break;
       ptx::fence_async_shared();
       ptx::tc_fence_before();
       ptx::mbar_arrive(p_full + (t & 1));
     }
     // the sums over the tokens: lanes, then warps, in a fixed order
-#pragma unroll
-    for (int c0 = 0; c0 < S::kCols; c0 += 16) {
-      float mine = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        float v = sum[c0 + k];
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == k) mine = v;
+    const float mine = over_lanes(sum, lane, [](float p, float q) { return p + q; });
+    if (lane % (32 / C) == 0) wstat[w4 * R + col0 + lane / (32 / C)] = mine;
+    group_sync(grp);
+    if (tok < C) {
+      const int c = col0 + tok, i = (row0 + c) / a.rep, h = row0 + c - i * a.rep;
+      const float l = (wstat[c] + wstat[R + c]) + (wstat[2 * R + c] + wstat[3 * R + c]);
+      const float lse2 = l == 0.f ? -INFINITY : ref[c] + log2f(l);
+      const int64_t row = sq.first + i, head = g * a.rep + h;
+      factor[c] = l == 0.f ? 0.f : 1.f / l;
+      int64_t z = -1;
+      if (i < sq.n) {
+        if (a.splits == 1) {
+          z = row * a.ldot + head * a.ldoh;
+          if (a.lse) a.lse[row * a.n_qh + head] = lse2 * kLn2;
+        } else {
+          z = (sp * a.rows + row) * a.n_qh + head;
+          a.part_lse[z] = lse2;
+          z *= D;
+        }
       }
-      if (lane < 16) wstat[w4 * R + col0 + c0 + lane] = mine;
+      place[c] = z;
     }
     group_sync(grp);
     if (nt > 0) {
@@ -584,9 +679,8 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
     }
     // out: thread = position tok of the head, one column after the other
     const int e = true_position<M>(tok);
-    const int64_t heads = a.n_qh;
-#pragma unroll
-    for (int c0 = 0; c0 < S::kCols; c0 += 16) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < C; c0 += 16) {
       float o[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) o[k] = 0.f;
@@ -600,31 +694,18 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
           for (int k = 0; k < 16; ++k) o[k] += __uint_as_float(r[k]);
         }
       }
-      int i = (row0 + col0 + c0) / a.rep, h = row0 + col0 + c0 - i * a.rep;
+      if (tok < D) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (i < sq.n) {
+        for (int k = 0; k < 16; ++k) {
           const int c = col0 + c0 + k;
-          const float l = wstat[c] + wstat[R + c] + wstat[2 * R + c] + wstat[3 * R + c];
-          const float y = l == 0.f ? 0.f : o[k] / l;
-          const int64_t row = sq.first + i, head = g * a.rep + h;
-          const float lse2 = l == 0.f ? -INFINITY : ref[c] + log2f(l);
-          if (a.splits == 1) {
-            if (tok < D) {
-              const int64_t z = row * a.ldot + head * a.ldoh + e;
-              if constexpr (FOUT) static_cast<float *>(a.out)[z] = y;
-              else static_cast<__nv_bfloat16 *>(a.out)[z] = __float2bfloat16(y);
-            }
-            if (a.lse && tok == 0) a.lse[row * heads + head] = lse2 * kLn2;
-          } else {
-            const int64_t z = (sp * a.rows + row) * heads + head;
-            if (tok < D) a.part[z * D + e] = y;
-            if (tok == 0) a.part_lse[z] = lse2;
-          }
-        }
-        if (++h == a.rep) {
-          h = 0;
-          ++i;
+          if (place[c] < 0) continue;
+          float y = o[k];
+          if (P > 1 && nt > kPeriod) y += acc[(c0 + k) * D];
+          y = factor[c] == 0.f ? 0.f : y * factor[c];
+          const int64_t z = place[c] + e;
+          if (a.splits > 1) a.part[z] = y;
+          else if constexpr (FOUT) static_cast<float *>(a.out)[z] = y;
+          else static_cast<__nv_bfloat16 *>(a.out)[z] = __float2bfloat16(y);
         }
       }
     }
@@ -632,7 +713,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == S::kSoftWarps + kDecodeWarps) ptx::tmem_dealloc(tmem, S::kTmem);
+  if (warp == 0) ptx::tmem_dealloc(tmem, S::kTmem);
 }
 
 // One warp per (drafted token, head): the splits' outputs, weighted by
