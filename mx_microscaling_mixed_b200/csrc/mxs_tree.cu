@@ -17,6 +17,8 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+struct Meta;
+
 struct TreeArgs {
   const uint16_t *q;
   int64_t ldqt, ldqh;
@@ -30,9 +32,15 @@ struct TreeArgs {
   void *out;
   int64_t ldot, ldoh;
   float *lse;
-  int32_t row_tiles, splits, tiles_per_split;
-  float *part, *part_lse;  // the splits' normalised outputs and base-2 lse: [split][row][head]([D])
+  int32_t row_tiles, ctas;
+  float *part, *part_lse;  // unfinished items' normalised outputs and base-2 lse: [CTA][first, last][column]([D])
+  Meta *meta;       // [CTA]; NULL where no item has more than one tile
   int *status;
+};
+
+// What a CTA says of its first item, for joining.
+struct Meta {
+  int b, rt, g, tile, tiles, total, parts, pad;
 };
 
 struct Sequence {
@@ -66,32 +74,47 @@ constexpr int kAtom = kTile * 128;               // 64 bf16 values of each token
 constexpr float kSlack = 24.f;                   // weights are kept below 2^kSlack
 constexpr long long kTreeWait = 2000000000LL;    // cycles (about 1 s)
 
-// R columns (query rows) per CTA; P bf16 pieces of a weight.
+// How a CTA's shared memory is laid out for R columns (query rows), P bf16
+// pieces of a weight: what has to be there once first, then a second place
+// for what waits most, while there is room.
 template <int D, int M, int R, int P>
 struct Shape {
-  static constexpr int kCols = R < 32 ? R : 32;          // columns of a softmax warp
-  static constexpr int kSoftWarps = R / kCols * 4;
-  static constexpr int kResident = R > 32 || (R == 32 && P > 1 && D > 64) ? 1 : 2;
-  static constexpr int kDecodeWarps = kResident == 1 ? 8 : 4;    // 8: four for K, four for V
-  static constexpr int kThreads = (kSoftWarps + kDecodeWarps) * 32;
-  static constexpr int kN = R * P;                       // columns of the output product
+  static constexpr int kSoftWarps = 8, kDecodeWarps = 8;     // two groups of four each
+  static constexpr int kMmaWarp = kSoftWarps + kDecodeWarps;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kCols = R / 2;                        // columns of a softmax group
+  static constexpr int kN = R * P;                           // columns of the output product
   static constexpr int kKV = kTile * D * 2;
-  static constexpr int kStages = kResident == 1 && R * P < 192 ? 2 : 1;    // of K and of V
-  static constexpr int kPWidth = R < 64 ? R : 64;        // columns in a row of a swizzle atom of the weights
+  static constexpr int kPWidth = R < 64 ? R : 64;            // columns in a row of a swizzle atom of the weights
   static constexpr int kPAtom = kTile * kPWidth * 2;
   static constexpr int kPBytes = kTile * kN * 2;
-  static constexpr int kPBufs = 2;
-  static constexpr int kK = 0, kV = kStages * kKV, kP = 2 * kStages * kKV, kQ = kP + kPBufs * kPBytes;
-  static constexpr int kAcc = kQ + R * D * 2;            // fp32 sums of output periods, [column][place]
-  static constexpr int kStat = kAcc + (P > 1 ? R * D * 4 : 0);   // per column: reference, factor, 4 maxima or sums
-  static constexpr int kPlace = kStat + 6 * R * 4;       // per column: where its output goes (64 bits)
+  static constexpr int kCodeRow = D * M / 8;                 // bytes
+  static constexpr int kRawTensor = kTile * (kCodeRow + 4);  // codes and scale words of a tile as fetched
+  static constexpr int kRaw = 2 * kRawTensor;
+  static constexpr int kQBytes = R * D * 2, kAccBytes = P > 1 ? R * D * 4 : 0;
+  static constexpr int kSmall = 6 * R * 4 + R * 8 + 16 * 8 + 256;
+  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall;
+  static constexpr int kOnce = 2 * kKV + kPBytes + kQBytes + kAccBytes + 2 * kRaw;
+  static constexpr bool kFits = kOnce <= kRoom;
+  static constexpr int kPBufs = kOnce + kPBytes <= kRoom ? 2 : 1;
+  static constexpr int kWithP = kOnce + (kPBufs - 1) * kPBytes;
+  static constexpr int kRings = kWithP + kRaw <= kRoom ? 3 : 2;          // fetched tiles
+  static constexpr int kWithRaw = kWithP + (kRings - 2) * kRaw;
+  static constexpr int kStagesK = kWithRaw + kKV <= kRoom ? 2 : 1;
+  static constexpr int kWithK = kWithRaw + (kStagesK - 1) * kKV;
+  static constexpr int kStagesV = kWithK + kKV <= kRoom ? 2 : 1;
+  static constexpr int kK = 0, kV = kStagesK * kKV, kP = kV + kStagesV * kKV, kQ = kP + kPBufs * kPBytes;
+  static constexpr int kAcc = kQ + kQBytes;                  // fp32 sums of output periods, [column][place]
+  static constexpr int kRawAt = kAcc + kAccBytes;
+  static constexpr int kStat = kRawAt + kRings * kRaw;       // per column: reference, factor, 4 maxima or sums
+  static constexpr int kPlace = kStat + 6 * R * 4;           // per column: where its output goes (64 bits)
   static constexpr int kBar = kPlace + R * 8;
-  static constexpr int kBars = kBar + (2 * kStages + 8) * 8 + 16;
-  // (heads of 64: the output product reads 64 places that nobody uses behind V's, which have to exist)
-  static constexpr int kEnd = kBars > kV + kStages * kKV + kAtom ? kBars : kV + kStages * kKV + kAtom;
+  static constexpr int kStart = kBar + 16 * 8;               // where the CTA's work begins
+  static constexpr int kEnd = kStart + 256;
   static constexpr int kBytes = kEnd + 1024;
+  // (heads of 64: the output product reads 64 places that nobody uses behind V's: P is there)
+  static_assert(kV + kStagesV * kKV + kAtom <= kEnd, "within the CTA's shared memory");
   static constexpr int kTmem = 2 * R + kN <= 64 ? 64 : 2 * R + kN <= 128 ? 128 : 2 * R + kN <= 256 ? 256 : 512;
-  static_assert(kResident * (kBytes + 1024) <= 228 * 1024 && kResident * kTmem <= 512, "the CTAs of an SM fit it");
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTile >> 4) << 24);
   static constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(R >> 3) << 17);
   static constexpr uint32_t kIdescO = kIdesc | (3u << 15) | (static_cast<uint32_t>(kN >> 3) << 17);
@@ -145,13 +168,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ uint4 load_stream(const uint8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
 }
 
 // bf16 bits of 2^(b - 129), the step of a 4-bit block with scale byte b.
@@ -267,77 +283,194 @@ __device__ __forceinline__ uint32_t seen_tokens(const TreeArgs &a, const Sequenc
   return limit >= 32 ? w : limit <= 0 ? 0u : w & ((1u << limit) - 1u);
 }
 
+// The tiles of a call in one line: row tile after row tile of sequence after
+// sequence, all K/V heads of each.  CTA c of n takes tiles c W / n up to
+// (c + 1) W / n of the W there are, whatever items they belong to; an item
+// that reaches over a CTA's end leaves partial results, joined afterwards.
+struct Walk {
+  int b, rt, g;              // the item
+  int tile, tiles;           // the first tile here and the item's tiles
+  int left;                  // tiles of the CTA from here on
+  Sequence sq;
+  TileRange range;
+  __device__ __forceinline__ int count() const { return min(tiles - tile, left); }
+  __device__ __forceinline__ bool whole() const { return tile == 0 && left >= tiles; }
+  __device__ __forceinline__ void load(const TreeArgs &a, int R) {
+    sq = sequence_of(a, b, false);
+    const bool rows = rt * R < sq.n * a.rep;
+    range = tile_range(a, sq, rt * R, R);
+    tiles = rows ? (range.total + kTile - 1) / kTile : 0;
+  }
+  __device__ __forceinline__ void next(const TreeArgs &a, int R) {
+    left -= count();
+    tile = 0;
+    if (left <= 0 || ++g < a.c.n_kvh) return;
+    g = 0;
+    do {
+      if (++rt == a.row_tiles) {
+        rt = 0;
+        if (++b == a.B) {
+          left = 0;          // (cannot be: the tiles were counted)
+          return;
+        }
+      }
+      load(a, R);
+    } while (tiles == 0);
+  }
+};
+__device__ __forceinline__ int first_tile(int64_t total, int parts, int c) { return static_cast<int>(total * c / parts); }
+
+// Finds the CTA's work: every thread counts the tiles of a stretch of (sequence,
+// row tile) pairs, one of them comes upon the CTA's first tile.
+template <int R, int THREADS>
+__device__ __forceinline__ void find_work(const TreeArgs &a, int *smem, Meta *meta) {
+  // smem: 8 ints of the result, then one per warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kWarps = THREADS / 32;
+  const int64_t pairs = static_cast<int64_t>(a.B) * a.row_tiles;
+  const int64_t per = (pairs + THREADS - 1) / THREADS;
+  const int64_t i0 = min(pairs, per * static_cast<int64_t>(threadIdx.x)), i1 = min(pairs, i0 + per);
+  Walk w;
+  int mine = 0;
+  for (int64_t i = i0; i < i1; ++i) {
+    w.b = static_cast<int>(i / a.row_tiles);
+    w.rt = static_cast<int>(i - static_cast<int64_t>(w.b) * a.row_tiles);
+    w.load(a, R);
+    mine += w.tiles * a.c.n_kvh;
+    if (blockIdx.x == 0 && w.rt == 0) sequence_of(a, w.b, true);
+  }
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) smem[8 + warp] = before;
+  if (threadIdx.x == 0) smem[0] = 0;                 // (no work unless found)
+  __syncthreads();
+  int total = 0, base = 0;
+#pragma unroll 1
+  for (int k = 0; k < kWarps; ++k) {
+    if (k == warp) base = total;
+    total += smem[8 + k];
+  }
+  before += base - mine;
+  const int parts = min(a.ctas, total);
+  if (static_cast<int>(blockIdx.x) < parts) {
+    const int begin = first_tile(total, parts, blockIdx.x), end = first_tile(total, parts, blockIdx.x + 1);
+    if (begin >= before && begin < before + mine) {
+      int at = before;
+      for (int64_t i = i0; i < i1; ++i) {
+        w.b = static_cast<int>(i / a.row_tiles);
+        w.rt = static_cast<int>(i - static_cast<int64_t>(w.b) * a.row_tiles);
+        w.load(a, R);
+        const int n = w.tiles * a.c.n_kvh;
+        if (begin < at + n) {
+          w.g = (begin - at) / w.tiles;
+          w.tile = begin - at - w.g * w.tiles;
+          smem[0] = end - begin;
+          smem[1] = w.b;
+          smem[2] = w.rt;
+          smem[3] = w.g;
+          smem[4] = w.tile;
+          if (meta) meta[blockIdx.x] = Meta{w.b, w.rt, w.g, w.tile, w.tiles, total, parts, 0};
+          break;
+        }
+        at += n;
+      }
+    }
+  } else if (threadIdx.x == 0 && meta) {
+    meta[blockIdx.x] = Meta{0, 0, 0, 0, 0, total, parts, 0};
+  }
+}
+__device__ __forceinline__ Walk start_walk(const TreeArgs &a, const int *smem, int R) {
+  Walk w;
+  w.left = smem[0];
+  w.b = smem[1];
+  w.rt = smem[2];
+  w.g = smem[3];
+  w.tile = smem[4];
+  w.tiles = 0;
+  if (w.left > 0) w.load(a, R);
+  return w;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 8) {
+    ptx::tmem_ld8(addr, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) ptx::tmem_ld16(addr + i, *reinterpret_cast<uint32_t(*)[16]>(&r[i]));
+  }
+  ptx::tmem_wait_ld();
+}
+
 }  // namespace
 
-// CTA = (sequence, kv head, split of the tokens, row tile).  Tokens are the
+// A persistent grid: CTA = a stretch of the line of tiles, one tile of 128
+// tokens of a (sequence, row tile, K/V head) after the other.  Tokens are the
 // 128 rows of the matrix instruction, query rows its columns, so that the
 // work follows the number of rows (16 to 64 of them) while a cache tile is
 // decoded once for all of them:
 //   S^T [token][row] = K Q^T     A = K  (token x d, K-major),  B = Q
 //   O^T [d][row]    += V^T P^T   A = V  (token x d, stored along d), B = P
-// Both accumulate in tensor memory.  Four or eight warps fetch and decode the
-// cache into shared memory, the first of K's and of V's issues the products;
-// four or eight turn scores into weights.  A softmax thread owns one token
-// and sums its weights per row over all tiles; the sums meet at the end.
+// Both accumulate in tensor memory.  Eight warps fetch (asynchronous copies,
+// tiles ahead) and decode the cache into shared memory, four K and four V;
+// one thread issues the products; eight warps turn scores into weights, four
+// for each half of the columns.  A softmax thread owns one token and sums its
+// weights per row over all tiles; the sums meet at an item's end.
 //   The running maximum of a row is a reference that weights are relative
-// to, common to all tokens: it is set by the first tile and moved only when
-// a score passes it by more than 24 (weights of 2^24), which fp32 and bf16 hold with no loss
-// of precision; so a tile usually needs no maximum over its tokens, only one
-// vote that none of its scores is above.
+// to, common to all tokens: it is set by an item's first tile and moved only
+// when a score passes it by more than 24 (weights of 2^24), which fp32 and
+// bf16 hold with no loss of precision; so a tile usually needs no maximum
+// over its tokens, only one vote that none of its scores is above.
 //   The tensor core's fp32 sums are rounded towards zero at every step: an
 // fp32 output is taken out of tensor memory every kPeriod tiles and summed
 // outside it.
 template <int D, int M, int R, int P, bool FOUT>
-__global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>::kResident) tree_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(TreeArgs a) {
   using S = Shape<D, M, R, P>;
-  constexpr int NS = S::kStages, C = S::kCols;
+  constexpr int C = S::kCols, SK = S::kStagesK, SV = S::kStagesV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float *ref = reinterpret_cast<float *>(smem + S::kStat), *factor = ref + R, *wstat = factor + R;   // wstat[4][R]
   int64_t *place = reinterpret_cast<int64_t *>(smem + S::kPlace);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::kBar);
-  uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *drained = bar + 6, *k_full = bar + 8, *v_full = k_full + NS;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(v_full + NS);
+  uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *k_full = bar + 6, *v_full = bar + 8, *drained = bar + 10;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 11);
   volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);
+  int *start = reinterpret_cast<int *>(smem + S::kStart);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_wait();
-  int x = blockIdx.x;
-  const int rt = x % a.row_tiles;
-  x /= a.row_tiles;
-  const int sp = x % a.splits;
-  x /= a.splits;
-  const int g = x % a.c.n_kvh, b = x / a.c.n_kvh;
-  const Sequence sq = sequence_of(a, b, rt == 0 && sp == 0 && g == 0 && threadIdx.x == 0);
-  const int row0 = rt * R;
-  const TileRange range = tile_range(a, sq, row0, R);
-  const int tile0 = sp * a.tiles_per_split;
-  const int nt = min(a.tiles_per_split, (range.total + kTile - 1) / kTile - tile0);
-  if (row0 >= sq.n * a.rep || (nt <= 0 && sp > 0)) {       // (split 0 writes the rows of an empty range)
-    pdl_trigger();
-    return;
-  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(k_full + i, 4 * 32);
       ptx::mbar_init(v_full + i, 4 * 32);
-    }
-    for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(s_done + i, 1);
       ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
       ptx::mbar_init(o_done + i, 1);
-      ptx::mbar_init(drained + i, 1);
     }
+    ptx::mbar_init(drained, 1);
     ptx::fence_mbar_init();
     *given_up = 0;
   }
   for (int i = threadIdx.x; i < R; i += S::kThreads) ref[i] = -INFINITY;
+  pdl_wait();
   // tensor memory is taken after the wait for earlier kernels and before
   // later ones may start: a CTA that waits for another kernel holds none
-  if (warp == 0) {
+  if (warp == S::kMmaWarp) {
     ptx::tmem_alloc(tmem_slot, S::kTmem);
     ptx::tmem_relinquish();
   }
+  find_work<R, S::kThreads>(a, start, a.meta);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -345,433 +478,463 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, Shape<D, M, R, P>
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_o = tmem + 2 * R;
   const uint32_t sbase = ptx::smem_addr(smem);
+  const int total = start[0];                        // the CTA's tiles; n counts them
 
-  if (warp >= S::kSoftWarps) {
-    // ------------------------------------ fetching, decoding, and the products
-    // Jobs are (tile, K or V): with four warps alternately K and V, with
-    // eight one of them per group.  Two jobs are on their way in registers.
-    constexpr bool kBoth = S::kDecodeWarps == 4;
-    constexpr int BL = D / kBlock;                   // blocks of a cache row
-    constexpr int kRows = 32 / BL;                   // rows per iteration of a warp
-    constexpr int kIt = 32 / kRows;
-    const int dw = warp - S::kSoftWarps, w = dw & 3;
-    const int own = dw >> 2;                         // (eight warps) 0: K, 1: V
-    const int q4 = lane >> 3, blk = q4 % BL;
-    const int row_in = w * 32 + (q4 / BL) * 8 + (lane & 7);
-    const uint32_t base = (blk / 2) * kAtom, chunk0 = (blk & 1) * 4;
-    const int jobs = nt <= 0 ? 0 : kBoth ? 2 * nt : nt;
-    uint4 raw[2][kIt][M / 4];
-    uint32_t sc[2][kIt];
-    int64_t at[kIt];
-    int page[kIt];
-    auto look_up = [&](int t) {                      // the pages of a tile
+  if (warp == S::kMmaWarp) {
+    // ------------------------------------------------------ matrix products
+    if (lane == 0 && total > 0) {
+      auto scores = [&](int n) {
+        if (!wait_phase(k_full + n % SK, (n / SK) & 1, given_up, a.status)) return false;
+        ptx::tc_fence_after();
+        const uint32_t kb = sbase + S::kK + (n % SK) * S::kKV;
 #pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int p = (tile0 + t) * kTile + it * kRows + row_in;
-        page[it] = t < nt && p < range.total ? a.pages[b * a.ldp + page_of(a, p)] : -1;
-      }
-    };
-    auto locate = [&](int t) {                       // its rows in the pool
+        for (int k = 0; k < D / 16; ++k)
+          ptx::mma_bf16(tmem + (n & 1) * R, ptx::desc_sw128(kb + (k / 4) * kAtom + (k % 4) * 32),
+                        ptx::desc_sw128(sbase + S::kQ + (k / 4) * (R * 128) + (k % 4) * 32), S::kIdescS, k > 0);
+        ptx::mma_commit(s_done + (n & 1));
+        return true;
+      };
+      Walk w = start_walk(a, start, R);
+      int n = 0;
+      bool ok = scores(0);
+      while (ok && w.left > 0) {
+        const int nt = w.count();
+        for (int t = 0; t < nt && ok; ++t, ++n) {
+          // (the scores of n + 1 go where those of n - 1 were: their weights have been waited for)
+          if (n + 1 < total) ok = scores(n + 1);
+          ok = ok && wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
+               wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const bool fresh = P > 1 ? t % kPeriod == 0 : t == 0;
+          const uint32_t vb = sbase + S::kV + (n % SV) * S::kKV, pb = sbase + S::kP + n % S::kPBufs * S::kPBytes;
 #pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const uint32_t p = (tile0 + t) * kTile + it * kRows + row_in;
-        const int64_t slot = static_cast<int64_t>(page[it]) * a.page_size + (p - page_of(a, p) * a.page_size);
-        const bool ok = page[it] >= 0 && slot < a.c.n_slots;
-        if (!ok && t < nt && static_cast<int>(p) < range.total) record_bad_index(a.status);
-        at[it] = ok ? slot * a.c.n_kvh + g : -1;
-      }
-    };
-    auto fetch = [&](int sv, int s) {
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        if (at[it] >= 0) {
-          const uint8_t *c = a.c.codes[sv] + at[it] * a.c.code_pitch[sv] + blk * (kBlock * M / 8);
-#pragma unroll
-          for (int i = 0; i < M / 4; ++i) raw[s][it][i] = load_stream(c + 16 * i);
-          sc[s][it] = __ldg(a.c.scales[sv] + at[it] * a.c.scale_pitch[sv] + blk);
-        } else {
-#pragma unroll
-          for (int i = 0; i < M / 4; ++i) raw[s][it][i] = make_uint4(0, 0, 0, 0);
-          sc[s][it] = 0;
+          for (int k = 0; k < kTile / 16; ++k)
+            ptx::mma_bf16(tmem_o, ptx::desc_mn<64>(vb + k * 2048, kAtom),
+                          ptx::desc_mn<S::kPWidth>(pb + k * 32 * S::kPWidth, S::kPAtom), S::kIdescO, !fresh || k > 0);
+          ptx::mma_commit(o_done + (n & 1));
         }
+        w.next(a, R);
       }
-    };
-    auto decode = [&](int s, uint32_t dst) {
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int r = it * kRows + row_in;
-        uint8_t *rowp = smem + dst + base + r * 128;
-        const BlockScale<M> bs(sc[s][it]);
-        const uint32_t *wd = reinterpret_cast<const uint32_t *>(&raw[s][it][0]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4 *>(rowp + (((chunk0 + j) ^ (r & 7)) << 4)) =
-              decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs);
+      if (!ok) {
+        // leave no product in flight: a last commit covers all that were issued
+        ptx::mma_commit(drained);
+        ptx::mbar_wait_cycles(drained, 0, kTreeWait);
       }
-      ptx::fence_async_shared();
-    };
-    auto scores = [&](int t) {                       // one lane: waits for K(t) and the place of its scores
-      bool ok = wait_phase(k_full + t % NS, (t / NS) & 1, given_up, a.status);
-      if (t >= 2) ok = ok && wait_phase(p_full + (t & 1), ((t - 2) >> 1) & 1, given_up, a.status);
-      if (!ok) return false;
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        ptx::mma_bf16(tmem + (t & 1) * R, ptx::desc_sw128(sbase + S::kK + (t % NS) * S::kKV + (k / 4) * kAtom + (k % 4) * 32),
-                      ptx::desc_sw128(sbase + S::kQ + (k / 4) * (R * 128) + (k % 4) * 32), S::kIdescS, k > 0);
-      ptx::mma_commit(s_done + (t & 1));
-      return true;
-    };
-    auto output = [&](int t) {                       // one lane: waits for V(t) and its weights
-      const bool ok = wait_phase(v_full + t % NS, (t / NS) & 1, given_up, a.status) &&
-                      wait_phase(p_full + (t & 1), (t >> 1) & 1, given_up, a.status);
-      if (!ok) return false;
-      ptx::tc_fence_after();
-      const bool fresh = P > 1 ? t % kPeriod == 0 : t == 0;
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        ptx::mma_bf16(tmem_o, ptx::desc_mn<64>(sbase + S::kV + (t % NS) * S::kKV + k * 2048, kAtom),
-                      ptx::desc_mn<S::kPWidth>(sbase + S::kP + t % S::kPBufs * S::kPBytes + k * 32 * S::kPWidth, S::kPAtom),
-                      S::kIdescO, !fresh || k > 0);
-      ptx::mma_commit(o_done + (t & 1));
-      return true;
-    };
-    // what the fetch of job j + 2 needs
-    auto advance = [&](int j) {
-      if (kBoth && (j & 1)) return;                  // V of the same tile
-      const int t = kBoth ? j >> 1 : j;
-      locate(t);
-      look_up(t + 1);
-    };
-    if (jobs > 0) {
-      look_up(0);
-      advance(0);
-      fetch(kBoth ? 0 : own, 0);
-      advance(1);
-      fetch(kBoth ? 1 : own, 1);
-      if (kBoth || own == 0) {
-        // q: row c of the tile, 16-byte chunks, zero where there is no such row
-        for (int i = (dw & 3) * 32 + lane; i < R * (D / 8); i += 128) {
-          const int c = i / (D / 8), e = i - c * (D / 8);
-          const int rr = row0 + c, di = rr / a.rep, h = rr - di * a.rep;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (di < sq.n)
-            v = *reinterpret_cast<const uint4 *>(a.q + (sq.first + di) * a.ldqt + (g * a.rep + h) * a.ldqh + e * 8);
-          *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) = reorder8<M>(v);
-        }
-      }
-    }
-    bool ok = true;
-    auto job = [&](int j, int s) {
-      const int t = kBoth ? j >> 1 : j;
-      const int isv = kBoth ? s : own;
-      const int u = t - NS;                          // the tile whose place this one takes
-      if (u >= 0) ok = wait_phase((isv ? o_done : s_done) + (u & 1), (u >> 1) & 1, given_up, a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      decode(s, (isv ? S::kV : S::kK) + (t % NS) * S::kKV);
-      ptx::mbar_arrive((isv ? v_full : k_full) + t % NS);
-      if (j + 2 < jobs) {
-        advance(j + 2);
-        fetch(isv, s);
-      }
-      if (w == 0) {
-        if (lane == 0) {
-          if (!isv) {
-            ok = scores(t);
-            if (kBoth && t > 0) ok = ok && output(t - 1);
-          } else if (!kBoth || t == nt - 1) {
-            ok = output(t);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      }
-    };
-    for (int j = 0; j < jobs && ok; j += 2) {
-      job(j, 0);
-      if (j + 1 < jobs && ok) job(j + 1, 1);
-    }
-    if (!ok && w == 0 && lane == 0) {
-      // leave no product in flight: a last commit covers all that this thread issued
-      ptx::mma_commit(drained + own);
-      ptx::mbar_wait_cycles(drained + own, 0, kTreeWait);
     }
     __syncwarp();
+  } else if (warp >= S::kSoftWarps) {
+    // ------------------------------------------------- fetching and decoding
+    // A warp has 32 rows of every tile of K or of V.  Copies of the next
+    // tiles are on their way into its own part of a ring.
+    constexpr int kRings = S::kRings;
+    constexpr int CR = S::kCodeRow, kChunks = CR / 16;       // 16-byte chunks of a row
+    constexpr int BL = D / kBlock;                           // blocks of a row
+    const int dw = warp - S::kSoftWarps, w4 = dw & 3, isv = dw >> 2;
+    const uint32_t raw = S::kRawAt + isv * S::kRawTensor + w4 * 32 * (CR + 4);
+    // chunk c of row r lies at chunk c ^ (r / (8 / kChunks)) % kChunks, so that 8 rows' meet no bank conflict
+    auto spot = [](int r, int c) { return r * CR + ((c ^ (r / (8 / kChunks)) % kChunks) << 4); };
+    const uint8_t *codes = a.c.codes[isv], *scales = a.c.scales[isv];
+    const int64_t code_pitch = a.c.code_pitch[isv], scale_pitch = a.c.scale_pitch[isv];
+
+    Walk f = start_walk(a, start, R);                        // of the tile looked up last
+    int ft = 0, page = -1, page_off = 0, page_g = 0;
+    bool there = false;
+    auto look_up = [&]() {                                   // the page of this lane's row of the next tile
+      there = false;
+      if (f.left <= 0) return;
+      const int p = (f.tile + ft) * kTile + w4 * 32 + lane;
+      page_g = f.g;
+      if (p < f.range.total) {
+        const uint32_t pg = page_of(a, p);
+        page = a.pages[f.b * a.ldp + pg];
+        page_off = static_cast<int>(p - pg * a.page_size);
+        there = true;
+      }
+      if (++ft == f.count()) {
+        ft = 0;
+        f.next(a, R);
+      }
+    };
+    auto fetch = [&](int n) {                                // copies of tile n, looked up before
+      const uint32_t to = sbase + raw + n % kRings * S::kRaw;
+      uint64_t row = ~uint64_t{0};
+      if (there) {
+        const int64_t slot = static_cast<int64_t>(page) * a.page_size + page_off;
+        if (page >= 0 && slot < a.c.n_slots) row = static_cast<uint64_t>(slot * a.c.n_kvh + page_g);
+        else record_bad_index(a.status);
+      }
+      const bool real = row != ~uint64_t{0};
+      copy4(to + 32 * CR + 4 * lane, scales + (real ? static_cast<int64_t>(row) * scale_pitch : 0), real);
+      const uint64_t addr = reinterpret_cast<uint64_t>(codes) + (real ? row * static_cast<uint64_t>(code_pitch) : 0);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+        const uint64_t from = __shfl_sync(0xffffffffu, addr, r);
+        const bool is = __shfl_sync(0xffffffffu, static_cast<int>(real), r);
+        copy16(to + spot(r, c), reinterpret_cast<const uint8_t *>(from) + 16 * c, is);
+      }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+    const int blk = (lane >> 3) % BL, row_in = (lane >> 3) / BL * 8 + (lane & 7);
+    constexpr int kRows = 32 / BL, kIt = BL;                 // rows per step of a warp, steps
+    const uint32_t base = (blk / 2) * kAtom, chunk0 = (blk & 1) * 4;
+    Walk w = start_walk(a, start, R);
+    look_up();
+#pragma unroll
+    for (int n = 0; n < kRings - 1; ++n) {
+      if (n < total) {
+        fetch(n);
+        look_up();
+      }
+      commit();
+    }
+    bool ok = true;
+    int n = 0;
+    while (ok && w.left > 0) {
+      const int nt = w.count();
+      for (int t = 0; t < nt; ++t, ++n) {
+        if (n + kRings - 1 < total) {
+          fetch(n + kRings - 1);
+          look_up();
+        }
+        commit();
+        constexpr int kQ = R * D / 8 / 128;                  // 16-byte chunks of q per thread of K's warps
+        uint4 qv[kQ];
+        if (t == 0 && !isv) {
+          // q of a new item: row c of the tile, zero where there is no such row
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            const int j = i * 128 + w4 * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+            const int rr = w.rt * R + c, di = rr / a.rep, h = rr - di * a.rep;
+            qv[i] = make_uint4(0, 0, 0, 0);
+            if (di < w.sq.n)
+              qv[i] = *reinterpret_cast<const uint4 *>(a.q + (w.sq.first + di) * a.ldqt + (w.g * a.rep + h) * a.ldqh + e * 8);
+          }
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRings - 1) : "memory");
+        __syncwarp();
+        // the place of tile u is taken; for a new q, every score of the old one has to be there
+        const int u = t == 0 && !isv ? n - 1 : n - (isv ? SV : SK);
+        if (u >= 0) ok = wait_phase((isv ? o_done : s_done) + (u & 1), (u >> 1) & 1, given_up, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (t == 0 && !isv) {
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            const int j = i * 128 + w4 * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+            *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) =
+                reorder8<M>(qv[i]);
+          }
+        }
+        const uint8_t *from = smem + raw + n % kRings * S::kRaw;
+        uint8_t *to = smem + (isv ? S::kV + n % SV * S::kKV : S::kK + n % SK * S::kKV) + base;
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const int r = it * kRows + row_in, rt = w4 * 32 + r;
+          uint4 code[M / 4];
+#pragma unroll
+          for (int i = 0; i < M / 4; ++i)
+            code[i] = *reinterpret_cast<const uint4 *>(from + spot(r, blk * (M / 4) + i));
+          const BlockScale<M> bs(from[32 * CR + 4 * r + blk]);
+          const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[0]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(to + rt * 128 + (((chunk0 + j) ^ (r & 7)) << 4)) =
+                decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs);
+        }
+        ptx::fence_async_shared();
+        ptx::mbar_arrive(isv ? v_full + n % SV : k_full + n % SK);
+        __syncwarp();                                        // (the ring's place may be written again)
+      }
+      if (ok) w.next(a, R);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     // -------------------------------------------------------------- softmax
     const int grp = warp >> 2, w4 = warp & 3;
     const int tok = w4 * 32 + lane, col0 = grp * C;
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    constexpr int CC = C < 16 ? C : 16;
     // the swizzle of a row of 128, 64 or 32 bytes
     const int pswz = S::kPWidth == 64 ? tok & 7 : S::kPWidth == 32 ? (tok >> 1) & 3 : (tok >> 2) & 1;
     float *acc = reinterpret_cast<float *>(smem + S::kAcc) + col0 * D + tok;
-    float sum[C];
+    const int e = true_position<M>(tok);
+    Walk w = start_walk(a, start, R);
+    bool ok = true, first = true;
+    int n = 0;
+    while (ok && w.left > 0) {
+      const int nt = w.count(), row0 = w.rt * R;
+      float sum[C];
 #pragma unroll
-    for (int k = 0; k < C; ++k) sum[k] = 0.f;
-    bool ok = true;
-    auto load_scores = [&](int t, uint32_t (&s)[C]) {
+      for (int k = 0; k < C; ++k) sum[k] = 0.f;
+      for (int t = 0; t < nt; ++t, ++n) {
+        ok = wait_phase(s_done + (n & 1), (n >> 1) & 1, given_up, a.status);
+        ptx::tc_fence_after();
+        uint32_t see = 0xFFFFFFFFu;
+        if ((w.tile + t + 1) * kTile > w.range.open) {
+          // lane k: column k's tokens of this warp, then exchanged
+          const int j0 = (w.tile + t) * kTile + w4 * 32 - w.sq.ctx;
+          const uint32_t mine = seen_tokens(a, w.sq, (row0 + col0 + lane % C) / a.rep, j0);
+          see = 0;
 #pragma unroll
-      for (int c0 = 0; c0 < C; c0 += 16)
-        ptx::tmem_ld16(tmem + lanes + (t & 1) * R + col0 + c0, *reinterpret_cast<uint32_t(*)[16]>(&s[c0]));
-      ptx::tmem_wait_ld();
-    };
-    for (int t = 0; t < nt; ++t) {
-      ok = wait_phase(s_done + (t & 1), (t >> 1) & 1, given_up, a.status);
-      ptx::tc_fence_after();
-      uint32_t see = 0xFFFFFFFFu;
-      if ((tile0 + t + 1) * kTile > range.open) {
-        // lane k: column k's tokens of this warp, then exchanged
-        const int j0 = (tile0 + t) * kTile + w4 * 32 - sq.ctx;
-        const uint32_t mine = seen_tokens(a, sq, (row0 + col0 + lane % C) / a.rep, j0);
-        see = 0;
-#pragma unroll
-        for (int k = 0; k < C; ++k) see |= (__shfl_sync(0xffffffffu, mine, k) >> lane & 1u) << k;
-      }
-      uint32_t s[C];
-      load_scores(t, s);
-      float v[C], top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < C; k += 4) {
-        const float4 r = *reinterpret_cast<const float4 *>(ref + col0 + k);
-        v[k] = fmaf(__uint_as_float(s[k]), a.scale_log2, -r.x);
-        v[k + 1] = fmaf(__uint_as_float(s[k + 1]), a.scale_log2, -r.y);
-        v[k + 2] = fmaf(__uint_as_float(s[k + 2]), a.scale_log2, -r.z);
-        v[k + 3] = fmaf(__uint_as_float(s[k + 3]), a.scale_log2, -r.w);
-      }
-      if (see != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
-      }
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        top = fmaxf(top, v[k]);
-        v[k] = exp2_fast(v[k]);
-      }
-      // (its vote below also carries a wait that ran out: all of the group leave together)
-      if (t >= S::kPBufs) {
-        const int u = t - S::kPBufs;
-        ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status) && ok;
-      }
-      const bool flush = P > 1 && t > 0 && t % kPeriod == 0;
-      if (any_of(grp, top > kSlack || !ok || flush)) {
-        // rare: a reference is overtaken (or not set yet), or an output period ends
-        if (t > 0 && ok) {
-          const int u = t - 1;
-          ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
-          ptx::tc_fence_after();
+          for (int k = 0; k < C; ++k) see |= (__shfl_sync(0xffffffffu, mine, k) >> lane & 1u) << k;
         }
-        if (any_of(grp, !ok)) {
-          ok = false;
-          break;
-        }
-        load_scores(t, s);
+        uint32_t s[C];
+        tmem_load(tmem + lanes + (n & 1) * R + col0, s);
+        float v[C], top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? __uint_as_float(s[k]) * a.scale_log2 : -INFINITY;
-        {
-          float m[C];
+        for (int k = 0; k < C; k += 4) {
+          const float4 r = *reinterpret_cast<const float4 *>(ref + col0 + k);
+          v[k] = fmaf(__uint_as_float(s[k]), a.scale_log2, -r.x);
+          v[k + 1] = fmaf(__uint_as_float(s[k + 1]), a.scale_log2, -r.y);
+          v[k + 2] = fmaf(__uint_as_float(s[k + 2]), a.scale_log2, -r.z);
+          v[k + 3] = fmaf(__uint_as_float(s[k + 3]), a.scale_log2, -r.w);
+        }
+        if (see != 0xFFFFFFFFu) {
 #pragma unroll
-          for (int k = 0; k < C; ++k) m[k] = v[k];
-          const float mine = over_lanes(m, lane, [](float p, float q) { return fmaxf(p, q); });
-          if (lane % (32 / C) == 0) wstat[w4 * R + col0 + lane / (32 / C)] = mine;
+          for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
         }
-        group_sync(grp);
-        if (tok < C) {
-          // references move only as far as they have to: by nothing, unless passed by 2^kSlack
-          const int c = col0 + tok;
-          const float old = ref[c];
-          float m = fmaxf(fmaxf(wstat[c], wstat[R + c]), fmaxf(wstat[2 * R + c], wstat[3 * R + c]));
-          m = m - old > kSlack || old == -INFINITY ? m : old;
-          factor[c] = m == old ? 1.f : exp2f(old - m);
-          ref[c] = m;
-        }
-        group_sync(grp);
 #pragma unroll
         for (int k = 0; k < C; ++k) {
-          sum[k] *= factor[col0 + k];
-          v[k] = (see >> k) & 1u ? exp2_fast(v[k] - ref[col0 + k]) : 0.f;
+          top = fmaxf(top, v[k]);
+          v[k] = exp2_fast(v[k]);
         }
-        if (t > 0) {
+        // (the vote below also carries a wait that ran out: all of the group leave together)
+        if (n >= S::kPBufs) {
+          const int u = n - S::kPBufs;
+          ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status) && ok;
+        }
+        const bool flush = P > 1 && t > 0 && t % kPeriod == 0;
+        if (any_of(grp, top > kSlack || !ok || flush)) {
+          // rare: a reference is overtaken (or not set yet), or an output period ends
+          if (t > 0 && ok) {
+            const int u = n - 1;
+            ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
+            ptx::tc_fence_after();
+          }
+          if (any_of(grp, !ok)) {
+            ok = false;
+            break;
+          }
+          tmem_load(tmem + lanes + (n & 1) * R + col0, s);
+#pragma unroll
+          for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? __uint_as_float(s[k]) * a.scale_log2 : -INFINITY;
+          {
+            float m[C];
+#pragma unroll
+            for (int k = 0; k < C; ++k) m[k] = v[k];
+            const float mine = over_lanes(m, lane, [](float p, float q) { return fmaxf(p, q); });
+            if (lane % (32 / C) == 0) wstat[w4 * R + col0 + lane / (32 / C)] = mine;
+          }
+          group_sync(grp);
+          if (tok < C) {
+            // references move only as far as they have to: by nothing, unless passed by 2^kSlack
+            const int c = col0 + tok;
+            const float old = ref[c];
+            float m = fmaxf(fmaxf(wstat[c], wstat[R + c]), fmaxf(wstat[2 * R + c], wstat[3 * R + c]));
+            m = m - old > kSlack || old == -INFINITY ? m : old;
+            factor[c] = m == old ? 1.f : exp2f(old - m);
+            ref[c] = m;
+          }
+          group_sync(grp);
+#pragma unroll
+          for (int k = 0; k < C; ++k) {
+            sum[k] *= factor[col0 + k];
+            v[k] = (see >> k) & 1u ? exp2_fast(v[k] - ref[col0 + k]) : 0.f;
+          }
+          if (t > 0) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            float part[16];
+            for (int c0 = 0; c0 < C; c0 += CC) {
+              float part[CC];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) part[k] = 0.f;
+              for (int k = 0; k < CC; ++k) part[k] = 0.f;
 #pragma unroll 1
-            for (int q = P - 1; q >= 0; --q) {
-              uint32_t o[16];
-              ptx::tmem_ld16(tmem_o + lanes + q * R + col0 + c0, o);
-              ptx::tmem_wait_ld();
-              if (flush) {
+              for (int q = P - 1; q >= 0; --q) {
+                uint32_t o[CC];
+                tmem_load(tmem_o + lanes + q * R + col0 + c0, o);
+                if (flush) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) part[k] += __uint_as_float(o[k]);
-              } else {
+                  for (int k = 0; k < CC; ++k) part[k] += __uint_as_float(o[k]);
+                } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor[col0 + c0 + k]);
-                ptx::tmem_st16(tmem_o + lanes + q * R + col0 + c0, o);
+                  for (int k = 0; k < CC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor[col0 + c0 + k]);
+                  if constexpr (CC == 8) ptx::tmem_st8(tmem_o + lanes + q * R + col0 + c0, o);
+                  else ptx::tmem_st16(tmem_o + lanes + q * R + col0 + c0, o);
+                }
+              }
+              if (P > 1 && tok < D && (flush || t > kPeriod)) {
+#pragma unroll
+                for (int k = 0; k < CC; ++k) {
+                  float *z = acc + (c0 + k) * D;
+                  *z = ((t > kPeriod ? *z : 0.f) + part[k]) * factor[col0 + c0 + k];
+                }
               }
             }
-            if (P > 1 && tok < D && (flush || t > kPeriod)) {
+            ptx::tmem_wait_st();
+          }
+          group_sync(grp);                           // (factor and wstat may be written again)
+        }
+        // the weights as P bf16 pieces, each the rounding of what the ones before left
+        uint8_t *prow = smem + S::kP + n % S::kPBufs * S::kPBytes + tok * (2 * S::kPWidth);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float *z = acc + (c0 + k) * D;
-                *z = ((t > kPeriod ? *z : 0.f) + part[k]) * factor[col0 + c0 + k];
+        for (int k = 0; k < C; ++k) sum[k] += v[k];
+#pragma unroll
+        for (int c0 = 0; c0 < C; c0 += 8) {
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[k] = pack2(v[c0 + 2 * k], v[c0 + 2 * k + 1]);
+              if (q + 1 < P) {
+                v[c0 + 2 * k] -= __uint_as_float(o[k] << 16);
+                v[c0 + 2 * k + 1] -= __uint_as_float(o[k] & 0xFFFF0000u);
               }
             }
+            const int cc = q * R + col0 + c0;
+            *reinterpret_cast<uint4 *>(prow + (cc / S::kPWidth) * S::kPAtom + (((cc % S::kPWidth) / 8 ^ pswz) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
           }
-          ptx::tmem_wait_st();
         }
-        group_sync(grp);                             // (factor and wstat may be written again)
+        ptx::fence_async_shared();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full + (n & 1));
       }
-      // the weights as P bf16 pieces, each the rounding of what the ones before left
-      uint8_t *prow = smem + S::kP + t % S::kPBufs * S::kPBytes + tok * (2 * S::kPWidth);
-#pragma unroll
-      for (int k = 0; k < C; ++k) sum[k] += v[k];
-#pragma unroll
-      for (int c0 = 0; c0 < C; c0 += 8) {
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[k] = pack2(v[c0 + 2 * k], v[c0 + 2 * k + 1]);
-            if (q + 1 < P) {
-              v[c0 + 2 * k] -= __uint_as_float(o[k] << 16);
-              v[c0 + 2 * k + 1] -= __uint_as_float(o[k] & 0xFFFF0000u);
-            }
+      if (!ok) break;
+      // the sums over the tokens: lanes, then warps, in a fixed order
+      const float mine = over_lanes(sum, lane, [](float p, float q) { return p + q; });
+      if (lane % (32 / C) == 0) wstat[w4 * R + col0 + lane / (32 / C)] = mine;
+      const bool whole = w.whole();
+      group_sync(grp);
+      if (tok < C) {
+        const int c = col0 + tok, i = (row0 + c) / a.rep, h = row0 + c - i * a.rep;
+        const float l = (wstat[c] + wstat[R + c]) + (wstat[2 * R + c] + wstat[3 * R + c]);
+        const float lse2 = l == 0.f ? -INFINITY : ref[c] + log2f(l);
+        const int64_t row = w.sq.first + i, head = w.g * a.rep + h;
+        factor[c] = l == 0.f ? 0.f : 1.f / l;
+        ref[c] = -INFINITY;
+        int64_t z = -1;
+        if (i < w.sq.n) {
+          if (whole) {
+            z = row * a.ldot + head * a.ldoh;
+            if (a.lse) a.lse[row * a.n_qh + head] = lse2 * kLn2;
+          } else {
+            // a CTA has at most two unfinished items, its first and its last
+            z = (static_cast<int64_t>(blockIdx.x) * 2 + !first) * R + c;
+            a.part_lse[z] = lse2;
+            z *= D;
           }
-          const int cc = q * R + col0 + c0;
-          *reinterpret_cast<uint4 *>(prow + (cc / S::kPWidth) * S::kPAtom + (((cc % S::kPWidth) / 8 ^ pswz) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
         }
+        place[c] = z;
       }
-      ptx::fence_async_shared();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(p_full + (t & 1));
-    }
-    // the sums over the tokens: lanes, then warps, in a fixed order
-    const float mine = over_lanes(sum, lane, [](float p, float q) { return p + q; });
-    if (lane % (32 / C) == 0) wstat[w4 * R + col0 + lane / (32 / C)] = mine;
-    group_sync(grp);
-    if (tok < C) {
-      const int c = col0 + tok, i = (row0 + c) / a.rep, h = row0 + c - i * a.rep;
-      const float l = (wstat[c] + wstat[R + c]) + (wstat[2 * R + c] + wstat[3 * R + c]);
-      const float lse2 = l == 0.f ? -INFINITY : ref[c] + log2f(l);
-      const int64_t row = sq.first + i, head = g * a.rep + h;
-      factor[c] = l == 0.f ? 0.f : 1.f / l;
-      int64_t z = -1;
-      if (i < sq.n) {
-        if (a.splits == 1) {
-          z = row * a.ldot + head * a.ldoh;
-          if (a.lse) a.lse[row * a.n_qh + head] = lse2 * kLn2;
-        } else {
-          z = (sp * a.rows + row) * a.n_qh + head;
-          a.part_lse[z] = lse2;
-          z *= D;
-        }
+      group_sync(grp);
+      {
+        const int u = n - 1;
+        ok = wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
+        ptx::tc_fence_after();
       }
-      place[c] = z;
-    }
-    group_sync(grp);
-    if (nt > 0) {
-      const int u = nt - 1;
-      ok = ok && wait_phase(o_done + (u & 1), (u >> 1) & 1, given_up, a.status);
-      ptx::tc_fence_after();
-    }
-    // out: thread = position tok of the head, one column after the other
-    const int e = true_position<M>(tok);
+      if (any_of(grp, !ok)) break;
+      // out: thread = position tok of the head, one column after the other
 #pragma unroll 1
-    for (int c0 = 0; c0 < C; c0 += 16) {
-      float o[16];
+      for (int c0 = 0; c0 < C; c0 += CC) {
+        float o[CC];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = 0.f;
-      if (nt > 0) {
+        for (int k = 0; k < CC; ++k) o[k] = 0.f;
 #pragma unroll
         for (int q = P - 1; q >= 0; --q) {
-          uint32_t r[16];
-          ptx::tmem_ld16(tmem_o + lanes + q * R + col0 + c0, r);
-          ptx::tmem_wait_ld();
+          uint32_t r[CC];
+          tmem_load(tmem_o + lanes + q * R + col0 + c0, r);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] += __uint_as_float(r[k]);
+          for (int k = 0; k < CC; ++k) o[k] += __uint_as_float(r[k]);
+        }
+        if (tok < D) {
+#pragma unroll
+          for (int k = 0; k < CC; ++k) {
+            const int c = col0 + c0 + k;
+            if (place[c] < 0) continue;
+            float y = o[k];
+            if (P > 1 && nt > kPeriod) y += acc[(c0 + k) * D];
+            y = factor[c] == 0.f ? 0.f : y * factor[c];
+            const int64_t z = place[c] + e;
+            if (!whole) a.part[z] = y;
+            else if constexpr (FOUT) static_cast<float *>(a.out)[z] = y;
+            else static_cast<__nv_bfloat16 *>(a.out)[z] = __float2bfloat16(y);
+          }
         }
       }
-      if (tok < D) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int c = col0 + c0 + k;
-          if (place[c] < 0) continue;
-          float y = o[k];
-          if (P > 1 && nt > kPeriod) y += acc[(c0 + k) * D];
-          y = factor[c] == 0.f ? 0.f : y * factor[c];
-          const int64_t z = place[c] + e;
-          if (a.splits > 1) a.part[z] = y;
-          else if constexpr (FOUT) static_cast<float *>(a.out)[z] = y;
-          else static_cast<__nv_bfloat16 *>(a.out)[z] = __float2bfloat16(y);
-        }
-      }
+      first = false;
+      w.next(a, R);
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 0) ptx::tmem_dealloc(tmem, S::kTmem);
+  if (warp == S::kMmaWarp) ptx::tmem_dealloc(tmem, S::kTmem);
 }
 
-// One warp per (drafted token, head): the splits' outputs, weighted by
-// 2^(lse_j - lse), in split order.
-template <int D, bool FOUT>
-__global__ void __launch_bounds__(128) tree_combine_kernel(TreeArgs a, int R) {
+// Joins an item's partial results, weighted by 2^(lse_j - lse) in the order
+// of the CTAs.  Block (c, chunk of 8 columns) takes the item that CTA c found
+// begun by the CTA before it, if that was the item's first; one warp a column.
+template <int D, int R, bool FOUT>
+__global__ void __launch_bounds__(256) tree_combine_kernel(TreeArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int E = D / 32;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int u = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int i = u / a.n_qh, head = u - i * a.n_qh;
-  const Sequence sq = sequence_of(a, b, false);
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const Meta m = a.meta[c];
+  if (c >= m.parts || m.tile == 0) return;
+  const int begin = first_tile(m.total, m.parts, c), before = begin - first_tile(m.total, m.parts, c - 1);
+  if (m.tile > before) return;                       // an earlier CTA began it
+  const int col = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Sequence sq = sequence_of(a, m.b, false);
+  const int i = (m.rt * R + col) / a.rep, h = m.rt * R + col - i * a.rep;
   if (i >= sq.n) return;
-  const int row0 = (i * a.rep + head % a.rep) / R * R;
-  const int tiles = (tile_range(a, sq, row0, R).total + kTile - 1) / kTile;
-  const int n = max(1, (tiles + a.tiles_per_split - 1) / a.tiles_per_split);
-  const int64_t row = sq.first + i, z0 = row * a.n_qh + head, step = a.rows * static_cast<int64_t>(a.n_qh);
-  float m = -INFINITY;
+  // parts: CTA c - 1 (its first or its last item), then the first items of c, c + 1, ... up to the item's end
+  const int64_t end = static_cast<int64_t>(begin) - m.tile + m.tiles;
+  int n = 2;
+  while (c + n - 1 < m.parts && first_tile(m.total, m.parts, c + n - 1) < end) ++n;
+  auto part_of = [&](int j) {
+    const int64_t slot = j == 0 ? (static_cast<int64_t>(c) - 1) * 2 + (m.tile < before) : (static_cast<int64_t>(c) + j - 1) * 2;
+    return slot * R + col;
+  };
+  float top = -INFINITY;
+  bool nan = false;
   for (int j = lane; j < n; j += 32) {
-    const float l = a.part_lse[z0 + j * step];
-    m = l == l ? fmaxf(m, l) : l;
-    if (m != m) break;
+    const float l = a.part_lse[part_of(j)];
+    nan |= l != l;
+    top = fmaxf(top, l);
   }
-  bool nan = m != m;
   nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float total = 0.f, acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (m != -INFINITY) {
+  for (int k = 0; k < E; ++k) acc[k] = 0.f;
+  if (top != -INFINITY) {
 #pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const float w = exp2f(a.part_lse[z0 + j * step] - m);
-      const float *p = a.part + (z0 + j * step) * D + lane * E;
+      const int64_t z = part_of(j);
+      const float w = exp2f(a.part_lse[z] - top);
+      const float *p = a.part + z * D + lane * E;
+      float v[E];
+      if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
+      else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
       total += w;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc[k] = fmaf(w, v[k], acc[k]);
     }
   }
+  const int64_t row = sq.first + i, head = m.g * a.rep + h;
   const float inv = nan ? NAN : total == 0.f ? 0.f : 1.f / total;
   const int64_t at = row * a.ldot + head * a.ldoh + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (FOUT) static_cast<float *>(a.out)[at + e] = acc[e] * inv;
-    else static_cast<__nv_bfloat16 *>(a.out)[at + e] = __float2bfloat16(acc[e] * inv);
+  for (int k = 0; k < E; ++k) {
+    if constexpr (FOUT) static_cast<float *>(a.out)[at + k] = acc[k] * inv;
+    else static_cast<__nv_bfloat16 *>(a.out)[at + k] = __float2bfloat16(acc[k] * inv);
   }
-  if (a.lse && lane == 0) a.lse[z0] = nan ? NAN : total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+  if (a.lse && lane == 0) a.lse[row * a.n_qh + head] = nan ? NAN : total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 namespace {
@@ -815,26 +978,31 @@ mxs_status tree_check(const mxs_kv_cache *cache, const mxs_tree_batch *t, int64_
   return MXS_OK;
 }
 
-// How a call is cut: columns of a row tile, row tiles, splits.
+// How a call is cut: columns of a row tile, row tiles, CTAs, and what
+// unfinished items need.  As many columns as a K/V group has rows, up to 64:
+// a cache tile is decoded once for all of them.  (An fp32 output's weights and
+// sums over an 8-bit cache of d = 128 leave shared memory for 32.)
 struct Cut {
   int R, pieces;
-  int64_t row_tiles, splits, tiles_per_split, part_bytes, lse_bytes;
+  int64_t row_tiles, tiles, ctas, part_bytes, lse_bytes, meta_bytes;
+  size_t bytes() const { return static_cast<size_t>(part_bytes + lse_bytes + meta_bytes); }
 };
 Cut tree_cut(const TreeArgs &a, bool fout, int sms) {
   Cut c{};
   c.pieces = fout ? 3 : 1;
   const int64_t group_rows = static_cast<int64_t>(a.max_q) * a.rep;
-  c.R = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : 64;
+  const int most = fout && a.c.d == 128 && a.c.bits == 8 ? 32 : 64;
+  c.R = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : most;
   c.row_tiles = (group_rows + c.R - 1) / c.R;
   const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(a.max_len) + kTile - 1) / kTile);
-  const int64_t base = c.row_tiles * a.c.n_kvh * a.B, room = 2 * sms;
-  const int64_t want = std::max<int64_t>(1, std::min(tiles, (room + base - 1) / base));
-  c.tiles_per_split = (tiles + want - 1) / want;
-  c.splits = (tiles + c.tiles_per_split - 1) / c.tiles_per_split;
-  if (c.splits > 1) {
-    const int64_t n = c.splits * a.rows * a.n_qh;
-    c.part_bytes = round_up(n * a.c.d * 4, 256);
-    c.lse_bytes = n * 4;
+  const __int128 all = static_cast<__int128>(tiles) * c.row_tiles * a.c.n_kvh * a.B;
+  c.tiles = all > INT32_MAX ? INT64_MAX : static_cast<int64_t>(all);
+  c.ctas = std::min<int64_t>(sms, c.tiles);
+  if (tiles > 1) {
+    const int64_t n = c.ctas * 2 * c.R;
+    c.part_bytes = n * a.c.d * 4;
+    c.lse_bytes = round_up(n * 4, 256);
+    c.meta_bytes = c.ctas * static_cast<int64_t>(sizeof(Meta));
   }
   return c;
 }
@@ -842,14 +1010,12 @@ Cut tree_cut(const TreeArgs &a, bool fout, int sms) {
 template <int D, int M, int R, int P, bool FOUT>
 mxs_status launch_tree(const TreeArgs &a, cudaStream_t s) {
   using S = Shape<D, M, R, P>;
+  static_assert(S::kFits && S::kBytes <= 227 * 1024, "a CTA's shared memory");
   if (!ensure_smem(tree_kernel<D, M, R, P, FOUT>, S::kBytes)) return MXS_ERR_CUDA;
-  const int64_t grid = static_cast<int64_t>(a.B) * a.c.n_kvh * a.splits * a.row_tiles;
-  launch_pdl(tree_kernel<D, M, R, P, FOUT>, dim3(static_cast<unsigned>(grid)), dim3(S::kThreads), S::kBytes, s, a);
+  launch_pdl(tree_kernel<D, M, R, P, FOUT>, dim3(static_cast<unsigned>(a.ctas)), dim3(S::kThreads), S::kBytes, s, a);
   count_launch();
-  if (a.splits > 1) {
-    const int64_t warps = static_cast<int64_t>(a.max_q) * a.n_qh;
-    launch_pdl(tree_combine_kernel<D, FOUT>, dim3(static_cast<unsigned>((warps + 3) / 4), static_cast<unsigned>(a.B)),
-               dim3(128), 0, s, a, R);
+  if (a.meta && a.ctas > 1) {
+    launch_pdl(tree_combine_kernel<D, R, FOUT>, dim3(static_cast<unsigned>(a.ctas - 1), R / 8), dim3(256), 0, s, a);
     count_launch();
   }
   return cuda_status(cudaGetLastError());
@@ -862,8 +1028,12 @@ mxs_status launch_shape(const TreeArgs &a, const Cut &c, cudaStream_t s) {
     return launch_tree<D, M, 64, 1, false>(a, s);
   }
   if (c.R == 16) return launch_tree<D, M, 16, 3, true>(a, s);
-  if (c.R == 32) return launch_tree<D, M, 32, 3, true>(a, s);
-  return launch_tree<D, M, 64, 3, true>(a, s);
+  if constexpr (D == 128 && M == 8) {
+    return launch_tree<D, M, 32, 3, true>(a, s);
+  } else {
+    if (c.R == 32) return launch_tree<D, M, 32, 3, true>(a, s);
+    return launch_tree<D, M, 64, 3, true>(a, s);
+  }
 }
 
 }  // namespace
@@ -879,7 +1049,7 @@ extern "C" mxs_status mxs_attn_tree_workspace_bytes(const mxs_kv_cache *cache, c
   const mxs_status st = tree_check(cache, batch, n_qh, &a);
   if (st != MXS_OK) return st;
   const Cut c = tree_cut(a, ot == MXS_F32, device_sms());
-  *bytes = static_cast<size_t>(c.part_bytes + c.lse_bytes);
+  *bytes = c.bytes();
   return MXS_OK;
 }
 
@@ -899,9 +1069,8 @@ extern "C" mxs_status mxs_attn_tree(const void *q, int64_t n_qh, int64_t ldqt, i
     return MXS_ERR_SHAPE;
   if (!aligned16(q) || ldqt % 8 || ldqh % 8) return MXS_ERR_ALIGN;
   const Cut c = tree_cut(a, ot == MXS_F32, device_sms());
-  if (static_cast<__int128>(a.B) * a.c.n_kvh * c.splits * c.row_tiles > INT32_MAX) return MXS_ERR_SHAPE;
-  if (c.splits > 1 && (!ws || ws_bytes < static_cast<size_t>(c.part_bytes + c.lse_bytes) ||
-                       (reinterpret_cast<uintptr_t>(ws) & 255u)))
+  if (c.tiles > INT32_MAX) return MXS_ERR_SHAPE;
+  if (c.bytes() > 0 && (!ws || ws_bytes < c.bytes() || (reinterpret_cast<uintptr_t>(ws) & 255u)))
     return MXS_ERR_WORKSPACE;
   if ((st = check_device()) != MXS_OK) return st;
   if (!(a.status = device_status_word())) return MXS_ERR_CUDA;
@@ -914,10 +1083,12 @@ extern "C" mxs_status mxs_attn_tree(const void *q, int64_t n_qh, int64_t ldqt, i
   a.ldoh = ldoh;
   a.lse = lse;
   a.row_tiles = static_cast<int32_t>(c.row_tiles);
-  a.splits = static_cast<int32_t>(c.splits);
-  a.tiles_per_split = static_cast<int32_t>(c.tiles_per_split);
-  a.part = static_cast<float *>(ws);
-  a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + c.part_bytes);
+  a.ctas = static_cast<int32_t>(c.ctas);
+  if (c.bytes() > 0) {
+    a.part = static_cast<float *>(ws);
+    a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + c.part_bytes);
+    a.meta = reinterpret_cast<Meta *>(static_cast<uint8_t *>(ws) + c.part_bytes + c.lse_bytes);
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d == 64) return a.c.bits == 4 ? launch_shape<64, 4>(a, c, s) : launch_shape<64, 8>(a, c, s);
   return a.c.bits == 4 ? launch_shape<128, 4>(a, c, s) : launch_shape<128, 8>(a, c, s);
