@@ -40,7 +40,9 @@ struct TreeArgs {
 
 // What a CTA says of its first item, for joining.
 struct Meta {
-  int b, rt, g, tile, tiles, total, parts, pad;
+  int first, n;            // the sequence's rows
+  int rt, g, tile, tiles;  // the item, its tile where the CTA begins, its tiles
+  int total, parts;        // tiles of the call, CTAs with work
 };
 
 struct Sequence {
@@ -80,8 +82,7 @@ constexpr long long kTreeWait = 2000000000LL;    // cycles (about 1 s)
 template <int D, int M, int R, int P>
 struct Shape {
   static constexpr int kSoftWarps = 8, kDecodeWarps = 8;     // two groups of four each
-  static constexpr int kMmaWarp = kSoftWarps + kDecodeWarps;
-  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kThreads = (kSoftWarps + kDecodeWarps) * 32;
   static constexpr int kCols = R / 2;                        // columns of a softmax group
   static constexpr int kN = R * P;                           // columns of the output product
   static constexpr int kKV = kTile * D * 2;
@@ -162,6 +163,24 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// (x, y) = (s, t) * scale + (r, q), two at once; s and t as bits.
+__device__ __forceinline__ void scale_shift(float &x, float &y, uint32_t s, uint32_t t, float scale, float r, float q) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(__uint_as_float(s)), "f"(__uint_as_float(t)), "f"(scale), "f"(r), "f"(q));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -284,9 +303,18 @@ __device__ __forceinline__ uint32_t seen_tokens(const TreeArgs &a, const Sequenc
 }
 
 // The tiles of a call in one line: row tile after row tile of sequence after
-// sequence, all K/V heads of each.  CTA c of n takes tiles c W / n up to
-// (c + 1) W / n of the W there are, whatever items they belong to; an item
-// that reaches over a CTA's end leaves partial results, joined afterwards.
+// sequence, all K/V heads of each.  The CTAs take equal stretches of it, of
+// whatever items they belong to; an item that reaches over a CTA's end leaves
+// partial results, joined afterwards.
+struct Stretch {
+  int size, more;            // tiles of a CTA, CTAs with one more
+  __device__ __forceinline__ Stretch(int total, int parts) : size(total / parts), more(total - size * parts) {}
+  __device__ __forceinline__ int begin(int c) const { return c * size + min(c, more); }
+  __device__ __forceinline__ int cta_of(int tile) const {
+    const int edge = more * (size + 1);
+    return tile < edge ? tile / (size + 1) : more + (tile - edge) / size;
+  }
+};
 struct Walk {
   int b, rt, g;              // the item
   int tile, tiles;           // the first tile here and the item's tiles
@@ -295,17 +323,15 @@ struct Walk {
   TileRange range;
   __device__ __forceinline__ int count() const { return min(tiles - tile, left); }
   __device__ __forceinline__ bool whole() const { return tile == 0 && left >= tiles; }
-  __device__ __forceinline__ void load(const TreeArgs &a, int R) {
-    sq = sequence_of(a, b, false);
-    const bool rows = rt * R < sq.n * a.rep;
+  __device__ __forceinline__ void measure(const TreeArgs &a, int R) {
     range = tile_range(a, sq, rt * R, R);
-    tiles = rows ? (range.total + kTile - 1) / kTile : 0;
+    tiles = rt * R < sq.n * a.rep ? (range.total + kTile - 1) / kTile : 0;
   }
-  __device__ __forceinline__ void next(const TreeArgs &a, int R) {
-    left -= count();
-    tile = 0;
-    if (left <= 0 || ++g < a.c.n_kvh) return;
-    g = 0;
+  __device__ __forceinline__ void load(const TreeArgs &a, int R, bool report) {
+    sq = sequence_of(a, b, report);
+    measure(a, R);
+  }
+  __device__ __forceinline__ void next_pair(const TreeArgs &a, int R) {
     do {
       if (++rt == a.row_tiles) {
         rt = 0;
@@ -314,31 +340,37 @@ struct Walk {
           return;
         }
       }
-      load(a, R);
+      load(a, R, false);
     } while (tiles == 0);
   }
+  __device__ __forceinline__ void next(const TreeArgs &a, int R) {
+    left -= count();
+    tile = 0;
+    if (left <= 0 || ++g < a.c.n_kvh) return;
+    g = 0;
+    next_pair(a, R);
+  }
 };
-__device__ __forceinline__ int first_tile(int64_t total, int parts, int c) { return static_cast<int>(total * c / parts); }
 
-// Finds the CTA's work: every thread counts the tiles of a stretch of (sequence,
+// Finds the CTA's work: every thread counts the tiles of a run of (sequence,
 // row tile) pairs, one of them comes upon the CTA's first tile.
 template <int R, int THREADS>
-__device__ __forceinline__ void find_work(const TreeArgs &a, int *smem, Meta *meta) {
+__device__ __forceinline__ void find_work(const TreeArgs &a, int *smem) {
   // smem: 8 ints of the result, then one per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kWarps = THREADS / 32;
-  const int64_t pairs = static_cast<int64_t>(a.B) * a.row_tiles;
-  const int64_t per = (pairs + THREADS - 1) / THREADS;
-  const int64_t i0 = min(pairs, per * static_cast<int64_t>(threadIdx.x)), i1 = min(pairs, i0 + per);
+  const uint32_t pairs = static_cast<uint32_t>(a.B) * a.row_tiles;
+  const uint32_t per = (pairs + THREADS - 1) / THREADS;
+  const uint32_t i0 = min(pairs, per * threadIdx.x), i1 = min(pairs, i0 + per);
   Walk w;
   int mine = 0;
-  for (int64_t i = i0; i < i1; ++i) {
+  auto take = [&](uint32_t i, bool report) {
     w.b = static_cast<int>(i / a.row_tiles);
-    w.rt = static_cast<int>(i - static_cast<int64_t>(w.b) * a.row_tiles);
-    w.load(a, R);
-    mine += w.tiles * a.c.n_kvh;
-    if (blockIdx.x == 0 && w.rt == 0) sequence_of(a, w.b, true);
-  }
+    w.rt = static_cast<int>(i - static_cast<uint32_t>(w.b) * a.row_tiles);
+    w.load(a, R, report && blockIdx.x == 0 && w.rt == 0);
+    return w.tiles * a.c.n_kvh;
+  };
+  for (uint32_t i = i0; i < i1; ++i) mine += take(i, true);
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -348,39 +380,40 @@ __device__ __forceinline__ void find_work(const TreeArgs &a, int *smem, Meta *me
   if (lane == 31) smem[8 + warp] = before;
   if (threadIdx.x == 0) smem[0] = 0;                 // (no work unless found)
   __syncthreads();
-  int total = 0, base = 0;
-#pragma unroll 1
-  for (int k = 0; k < kWarps; ++k) {
-    if (k == warp) base = total;
-    total += smem[8 + k];
+  int sums = lane < kWarps ? smem[8 + lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += v;
   }
-  before += base - mine;
+  const int total = __shfl_sync(0xffffffffu, sums, 31);
+  const int earlier = __shfl_sync(0xffffffffu, sums, max(warp - 1, 0));
+  before += (warp > 0 ? earlier : 0) - mine;
   const int parts = min(a.ctas, total);
   if (static_cast<int>(blockIdx.x) < parts) {
-    const int begin = first_tile(total, parts, blockIdx.x), end = first_tile(total, parts, blockIdx.x + 1);
+    const Stretch st(total, parts);
+    const int begin = st.begin(blockIdx.x);
     if (begin >= before && begin < before + mine) {
-      int at = before;
-      for (int64_t i = i0; i < i1; ++i) {
-        w.b = static_cast<int>(i / a.row_tiles);
-        w.rt = static_cast<int>(i - static_cast<int64_t>(w.b) * a.row_tiles);
-        w.load(a, R);
-        const int n = w.tiles * a.c.n_kvh;
-        if (begin < at + n) {
-          w.g = (begin - at) / w.tiles;
-          w.tile = begin - at - w.g * w.tiles;
-          smem[0] = end - begin;
-          smem[1] = w.b;
-          smem[2] = w.rt;
-          smem[3] = w.g;
-          smem[4] = w.tile;
-          if (meta) meta[blockIdx.x] = Meta{w.b, w.rt, w.g, w.tile, w.tiles, total, parts, 0};
-          break;
-        }
+      int at = before, n = mine;
+      for (uint32_t i = i0; i < i1; ++i) {
+        if (per > 1) n = take(i, false);
+        if (begin < at + n) break;
         at += n;
       }
+      w.g = (begin - at) / w.tiles;
+      w.tile = begin - at - w.g * w.tiles;
+      smem[0] = st.begin(blockIdx.x + 1) - begin;
+      smem[1] = w.b;
+      smem[2] = w.rt;
+      smem[3] = w.g;
+      smem[4] = w.tile;
+      smem[5] = w.sq.first;
+      smem[6] = w.sq.n;
+      smem[7] = w.sq.ctx;
+      if (a.meta) a.meta[blockIdx.x] = Meta{w.sq.first, w.sq.n, w.rt, w.g, w.tile, w.tiles, total, parts};
     }
-  } else if (threadIdx.x == 0 && meta) {
-    meta[blockIdx.x] = Meta{0, 0, 0, 0, 0, total, parts, 0};
+  } else if (threadIdx.x == 0 && a.meta) {
+    a.meta[blockIdx.x] = Meta{0, 0, 0, 0, 0, 0, total, parts};
   }
 }
 __device__ __forceinline__ Walk start_walk(const TreeArgs &a, const int *smem, int R) {
@@ -390,8 +423,9 @@ __device__ __forceinline__ Walk start_walk(const TreeArgs &a, const int *smem, i
   w.rt = smem[2];
   w.g = smem[3];
   w.tile = smem[4];
+  w.sq = Sequence{smem[5], smem[6], smem[7]};
   w.tiles = 0;
-  if (w.left > 0) w.load(a, R);
+  if (w.left > 0) w.measure(a, R);
   return w;
 }
 
@@ -424,8 +458,8 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 //   O^T [d][row]    += V^T P^T   A = V  (token x d, stored along d), B = P
 // Both accumulate in tensor memory.  Eight warps fetch (asynchronous copies,
 // tiles ahead) and decode the cache into shared memory, four K and four V;
-// one thread issues the products; eight warps turn scores into weights, four
-// for each half of the columns.  A softmax thread owns one token and sums its
+// one lane of each issues its products; eight warps turn scores into weights,
+// four for each half of the columns.  A softmax thread owns one token and sums its
 // weights per row over all tiles; the sums meet at an item's end.
 //   The running maximum of a row is a reference that weights are relative
 // to, common to all tokens: it is set by an item's first tile and moved only
@@ -441,11 +475,12 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   constexpr int C = S::kCols, SK = S::kStagesK, SV = S::kStagesV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (ref: the references, negated)
   float *ref = reinterpret_cast<float *>(smem + S::kStat), *factor = ref + R, *wstat = factor + R;   // wstat[4][R]
   int64_t *place = reinterpret_cast<int64_t *>(smem + S::kPlace);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::kBar);
   uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *k_full = bar + 6, *v_full = bar + 8, *drained = bar + 10;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 11);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 12);
   volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);
   int *start = reinterpret_cast<int *>(smem + S::kStart);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -457,20 +492,20 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       ptx::mbar_init(s_done + i, 1);
       ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
       ptx::mbar_init(o_done + i, 1);
+      ptx::mbar_init(drained + i, 1);
     }
-    ptx::mbar_init(drained, 1);
     ptx::fence_mbar_init();
     *given_up = 0;
   }
-  for (int i = threadIdx.x; i < R; i += S::kThreads) ref[i] = -INFINITY;
+  for (int i = threadIdx.x; i < R; i += S::kThreads) ref[i] = INFINITY;
   pdl_wait();
   // tensor memory is taken after the wait for earlier kernels and before
   // later ones may start: a CTA that waits for another kernel holds none
-  if (warp == S::kMmaWarp) {
+  if (warp == 0) {
     ptx::tmem_alloc(tmem_slot, S::kTmem);
     ptx::tmem_relinquish();
   }
-  find_work<R, S::kThreads>(a, start, a.meta);
+  find_work<R, S::kThreads>(a, start);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -480,124 +515,115 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   const uint32_t sbase = ptx::smem_addr(smem);
   const int total = start[0];                        // the CTA's tiles; n counts them
 
-  if (warp == S::kMmaWarp) {
-    // ------------------------------------------------------ matrix products
-    if (lane == 0 && total > 0) {
-      auto scores = [&](int n) {
-        if (!wait_phase(k_full + n % SK, (n / SK) & 1, given_up, a.status)) return false;
-        ptx::tc_fence_after();
-        const uint32_t kb = sbase + S::kK + (n % SK) * S::kKV;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          ptx::mma_bf16(tmem + (n & 1) * R, ptx::desc_sw128(kb + (k / 4) * kAtom + (k % 4) * 32),
-                        ptx::desc_sw128(sbase + S::kQ + (k / 4) * (R * 128) + (k % 4) * 32), S::kIdescS, k > 0);
-        ptx::mma_commit(s_done + (n & 1));
-        return true;
-      };
-      Walk w = start_walk(a, start, R);
-      int n = 0;
-      bool ok = scores(0);
-      while (ok && w.left > 0) {
-        const int nt = w.count();
-        for (int t = 0; t < nt && ok; ++t, ++n) {
-          // (the scores of n + 1 go where those of n - 1 were: their weights have been waited for)
-          if (n + 1 < total) ok = scores(n + 1);
-          ok = ok && wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
-               wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const bool fresh = P > 1 ? t % kPeriod == 0 : t == 0;
-          const uint32_t vb = sbase + S::kV + (n % SV) * S::kKV, pb = sbase + S::kP + n % S::kPBufs * S::kPBytes;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            ptx::mma_bf16(tmem_o, ptx::desc_mn<64>(vb + k * 2048, kAtom),
-                          ptx::desc_mn<S::kPWidth>(pb + k * 32 * S::kPWidth, S::kPAtom), S::kIdescO, !fresh || k > 0);
-          ptx::mma_commit(o_done + (n & 1));
-        }
-        w.next(a, R);
-      }
-      if (!ok) {
-        // leave no product in flight: a last commit covers all that were issued
-        ptx::mma_commit(drained);
-        ptx::mbar_wait_cycles(drained, 0, kTreeWait);
-      }
-    }
-    __syncwarp();
-  } else if (warp >= S::kSoftWarps) {
-    // ------------------------------------------------- fetching and decoding
+  if (warp >= S::kSoftWarps) {
+    // ------------------------------------------------- fetching, decoding, the products
     // A warp has 32 rows of every tile of K or of V.  Copies of the next
-    // tiles are on their way into its own part of a ring.
+    // tiles are on their way into its own part of a ring.  The first warp of
+    // each four issues the products that take what they decode, by one lane.
     constexpr int kRings = S::kRings;
     constexpr int CR = S::kCodeRow, kChunks = CR / 16;       // 16-byte chunks of a row
     constexpr int BL = D / kBlock;                           // blocks of a row
     const int dw = warp - S::kSoftWarps, w4 = dw & 3, isv = dw >> 2;
     const uint32_t raw = S::kRawAt + isv * S::kRawTensor + w4 * 32 * (CR + 4);
     // chunk c of row r lies at chunk c ^ (r / (8 / kChunks)) % kChunks, so that 8 rows' meet no bank conflict
-    auto spot = [](int r, int c) { return r * CR + ((c ^ (r / (8 / kChunks)) % kChunks) << 4); };
     const uint8_t *codes = a.c.codes[isv], *scales = a.c.scales[isv];
     const int64_t code_pitch = a.c.code_pitch[isv], scale_pitch = a.c.scale_pitch[isv];
 
+    struct Look {
+      int page, off, g;                                      // page: -2 where there is no such token
+    };
     Walk f = start_walk(a, start, R);                        // of the tile looked up last
-    int ft = 0, page = -1, page_off = 0, page_g = 0;
-    bool there = false;
+    int ft = 0;
     auto look_up = [&]() {                                   // the page of this lane's row of the next tile
-      there = false;
-      if (f.left <= 0) return;
+      Look k{-2, 0, f.g};
+      if (f.left <= 0) return k;
       const int p = (f.tile + ft) * kTile + w4 * 32 + lane;
-      page_g = f.g;
       if (p < f.range.total) {
         const uint32_t pg = page_of(a, p);
-        page = a.pages[f.b * a.ldp + pg];
-        page_off = static_cast<int>(p - pg * a.page_size);
-        there = true;
+        k.page = max(a.pages[f.b * a.ldp + pg], -1);
+        k.off = static_cast<int>(p - pg * a.page_size);
       }
       if (++ft == f.count()) {
         ft = 0;
         f.next(a, R);
       }
+      return k;
     };
-    auto fetch = [&](int n) {                                // copies of tile n, looked up before
+    const int in8 = lane / kChunks, swz = (in8 & 7) / (8 / kChunks) % kChunks;
+    auto fetch = [&](int n, const Look &k) {                 // copies of tile n, looked up before
       const uint32_t to = sbase + raw + n % kRings * S::kRaw;
-      uint64_t row = ~uint64_t{0};
-      if (there) {
-        const int64_t slot = static_cast<int64_t>(page) * a.page_size + page_off;
-        if (page >= 0 && slot < a.c.n_slots) row = static_cast<uint64_t>(slot * a.c.n_kvh + page_g);
-        else record_bad_index(a.status);
-      }
-      const bool real = row != ~uint64_t{0};
-      copy4(to + 32 * CR + 4 * lane, scales + (real ? static_cast<int64_t>(row) * scale_pitch : 0), real);
-      const uint64_t addr = reinterpret_cast<uint64_t>(codes) + (real ? row * static_cast<uint64_t>(code_pitch) : 0);
+      const int64_t slot = static_cast<int64_t>(k.page) * a.page_size + k.off;
+      const bool real = k.page >= 0 && slot < a.c.n_slots;
+      if (!real && k.page != -2) record_bad_index(a.status);
+      const int64_t row = real ? slot * a.c.n_kvh + k.g : 0;
+      copy4(to + 32 * CR + 4 * lane, scales + row * scale_pitch, real);
+      // (the lowest bit of an address says that the row is there)
+      const uint64_t addr = reinterpret_cast<uint64_t>(codes) + static_cast<uint64_t>(row * code_pitch) + real;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
-        const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
-        const uint64_t from = __shfl_sync(0xffffffffu, addr, r);
-        const bool is = __shfl_sync(0xffffffffu, static_cast<int>(real), r);
-        copy16(to + spot(r, c), reinterpret_cast<const uint8_t *>(from) + 16 * c, is);
+        // rows lane / kChunks of the i-th 32 / kChunks rows, chunk lane % kChunks
+        const int rr = i * (32 / kChunks) + in8, c = lane % kChunks;
+        const int sw = kChunks == 8 ? ((i & 1) * 4 + in8) & 7 : swz;
+        const uint64_t from = __shfl_sync(0xffffffffu, addr, rr);
+        copy16(to + rr * CR + ((c ^ sw) << 4), reinterpret_cast<const uint8_t *>(from & ~uint64_t{1}) + 16 * c, from & 1);
       }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
     const int blk = (lane >> 3) % BL, row_in = (lane >> 3) / BL * 8 + (lane & 7);
     constexpr int kRows = 32 / BL, kIt = BL;                 // rows per step of a warp, steps
-    const uint32_t base = (blk / 2) * kAtom, chunk0 = (blk & 1) * 4;
+    // where this lane reads and writes: rows step by multiples of 8, the swizzles stay
+    const int r8 = lane & 7;
+    uint32_t src[M / 4], dst[4];
+#pragma unroll
+    for (int i = 0; i < M / 4; ++i) src[i] = row_in * CR + ((blk * (M / 4) + i ^ (r8 / (8 / kChunks)) % kChunks) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = (blk / 2) * kAtom + (w4 * 32 + row_in) * 128 + (((blk & 1) * 4 + i ^ r8) << 4);
+    auto scores = [&](int n) {                               // waits for K(n) and for the place of its scores
+      bool ok = wait_phase(k_full + n % SK, (n / SK) & 1, given_up, a.status);
+      if (n >= 2) ok = ok && wait_phase(p_full + (n & 1), ((n - 2) >> 1) & 1, given_up, a.status);
+      if (!ok) return false;
+      ptx::tc_fence_after();
+      const uint64_t kd = ptx::desc_sw128(sbase + S::kK + (n % SK) * S::kKV), qd = ptx::desc_sw128(sbase + S::kQ);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        ptx::mma_bf16(tmem + (n & 1) * R, kd + (((k / 4) * kAtom + (k % 4) * 32) >> 4),
+                      qd + (((k / 4) * (R * 128) + (k % 4) * 32) >> 4), S::kIdescS, k > 0);
+      ptx::mma_commit(s_done + (n & 1));
+      return true;
+    };
+    auto output = [&](int n, int t) {                        // waits for V(n) and its weights
+      const bool ok = wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
+                      wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
+      if (!ok) return false;
+      ptx::tc_fence_after();
+      const bool fresh = P > 1 ? t % kPeriod == 0 : t == 0;
+      const uint64_t vd = ptx::desc_mn<64>(sbase + S::kV + (n % SV) * S::kKV, kAtom);
+      const uint64_t pd = ptx::desc_mn<S::kPWidth>(sbase + S::kP + n % S::kPBufs * S::kPBytes, S::kPAtom);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        ptx::mma_bf16(tmem_o, vd + k * (2048 >> 4), pd + k * (32 * S::kPWidth >> 4), S::kIdescO, !fresh || k > 0);
+      ptx::mma_commit(o_done + (n & 1));
+      return true;
+    };
     Walk w = start_walk(a, start, R);
-    look_up();
+    Look ahead[kRings];
+#pragma unroll
+    for (int n = 0; n < kRings; ++n) ahead[n] = look_up();
 #pragma unroll
     for (int n = 0; n < kRings - 1; ++n) {
-      if (n < total) {
-        fetch(n);
-        look_up();
-      }
+      if (n < total) fetch(n, ahead[n]);
       commit();
     }
+    Look next = ahead[kRings - 1];
     bool ok = true;
-    int n = 0;
+    int n = 0, t_before = 0;
     while (ok && w.left > 0) {
       const int nt = w.count();
       for (int t = 0; t < nt; ++t, ++n) {
         if (n + kRings - 1 < total) {
-          fetch(n + kRings - 1);
-          look_up();
+          fetch(n + kRings - 1, next);
+          next = look_up();
         }
         commit();
         constexpr int kQ = R * D / 8 / 128;                  // 16-byte chunks of q per thread of K's warps
@@ -629,27 +655,45 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
           }
         }
         const uint8_t *from = smem + raw + n % kRings * S::kRaw;
-        uint8_t *to = smem + (isv ? S::kV + n % SV * S::kKV : S::kK + n % SK * S::kKV) + base;
+        uint8_t *to = smem + (isv ? S::kV + n % SV * S::kKV : S::kK + n % SK * S::kKV);
 #pragma unroll
         for (int it = 0; it < kIt; ++it) {
-          const int r = it * kRows + row_in, rt = w4 * 32 + r;
           uint4 code[M / 4];
 #pragma unroll
-          for (int i = 0; i < M / 4; ++i)
-            code[i] = *reinterpret_cast<const uint4 *>(from + spot(r, blk * (M / 4) + i));
-          const BlockScale<M> bs(from[32 * CR + 4 * r + blk]);
+          for (int i = 0; i < M / 4; ++i) code[i] = *reinterpret_cast<const uint4 *>(from + src[i] + it * kRows * CR);
+          const BlockScale<M> bs(from[32 * CR + 4 * row_in + blk + it * kRows * 4]);
           const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(to + rt * 128 + (((chunk0 + j) ^ (r & 7)) << 4)) =
+            *reinterpret_cast<uint4 *>(to + dst[j] + it * kRows * 128) =
                 decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs);
         }
         ptx::fence_async_shared();
         ptx::mbar_arrive(isv ? v_full + n % SV : k_full + n % SK);
         __syncwarp();                                        // (the ring's place may be written again)
+        if (w4 == 0) {
+          // V's second place lets its warps decode on while the weights are made: the product before this one then
+          if (lane == 0) {
+            if (!isv) ok = scores(n);
+            else if (SV == 1) ok = output(n, t);
+            else if (n > 0) ok = output(n - 1, t_before);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          t_before = t;
+          if (!ok) break;
+        }
       }
       if (ok) w.next(a, R);
     }
+    if (w4 == 0 && lane == 0 && total > 0) {
+      if (ok && isv && SV > 1) ok = output(total - 1, t_before);
+      if (!ok) {
+        // leave no product in flight: a last commit covers all that this thread issued
+        ptx::mma_commit(drained + isv);
+        ptx::mbar_wait_cycles(drained + isv, 0, kTreeWait);
+      }
+    }
+    __syncwarp();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     // -------------------------------------------------------------- softmax
@@ -687,20 +731,17 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
 #pragma unroll
         for (int k = 0; k < C; k += 4) {
           const float4 r = *reinterpret_cast<const float4 *>(ref + col0 + k);
-          v[k] = fmaf(__uint_as_float(s[k]), a.scale_log2, -r.x);
-          v[k + 1] = fmaf(__uint_as_float(s[k + 1]), a.scale_log2, -r.y);
-          v[k + 2] = fmaf(__uint_as_float(s[k + 2]), a.scale_log2, -r.z);
-          v[k + 3] = fmaf(__uint_as_float(s[k + 3]), a.scale_log2, -r.w);
+          scale_shift(v[k], v[k + 1], s[k], s[k + 1], a.scale_log2, r.x, r.y);
+          scale_shift(v[k + 2], v[k + 3], s[k + 2], s[k + 3], a.scale_log2, r.z, r.w);
         }
         if (see != 0xFFFFFFFFu) {
 #pragma unroll
           for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
         }
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-          top = fmaxf(top, v[k]);
-          v[k] = exp2_fast(v[k]);
-        }
+        for (int k = 0; k < C; k += 2) top = max3(top, v[k], v[k + 1]);
+#pragma unroll
+        for (int k = 0; k < C; ++k) v[k] = exp2_fast(v[k]);
         // (the vote below also carries a wait that ran out: all of the group leave together)
         if (n >= S::kPBufs) {
           const int u = n - S::kPBufs;
@@ -732,17 +773,17 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
           if (tok < C) {
             // references move only as far as they have to: by nothing, unless passed by 2^kSlack
             const int c = col0 + tok;
-            const float old = ref[c];
+            const float old = -ref[c];
             float m = fmaxf(fmaxf(wstat[c], wstat[R + c]), fmaxf(wstat[2 * R + c], wstat[3 * R + c]));
             m = m - old > kSlack || old == -INFINITY ? m : old;
             factor[c] = m == old ? 1.f : exp2f(old - m);
-            ref[c] = m;
+            ref[c] = -m;
           }
           group_sync(grp);
 #pragma unroll
           for (int k = 0; k < C; ++k) {
             sum[k] *= factor[col0 + k];
-            v[k] = (see >> k) & 1u ? exp2_fast(v[k] - ref[col0 + k]) : 0.f;
+            v[k] = (see >> k) & 1u ? exp2_fast(v[k] + ref[col0 + k]) : 0.f;
           }
           if (t > 0) {
 #pragma unroll 1
@@ -779,7 +820,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
         // the weights as P bf16 pieces, each the rounding of what the ones before left
         uint8_t *prow = smem + S::kP + n % S::kPBufs * S::kPBytes + tok * (2 * S::kPWidth);
 #pragma unroll
-        for (int k = 0; k < C; ++k) sum[k] += v[k];
+        for (int k = 0; k < C; k += 2) add2(sum[k], sum[k + 1], v[k], v[k + 1]);
 #pragma unroll
         for (int c0 = 0; c0 < C; c0 += 8) {
 #pragma unroll
@@ -811,10 +852,10 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       if (tok < C) {
         const int c = col0 + tok, i = (row0 + c) / a.rep, h = row0 + c - i * a.rep;
         const float l = (wstat[c] + wstat[R + c]) + (wstat[2 * R + c] + wstat[3 * R + c]);
-        const float lse2 = l == 0.f ? -INFINITY : ref[c] + log2f(l);
+        const float lse2 = l == 0.f ? -INFINITY : log2f(l) - ref[c];
         const int64_t row = w.sq.first + i, head = w.g * a.rep + h;
         factor[c] = l == 0.f ? 0.f : 1.f / l;
-        ref[c] = -INFINITY;
+        ref[c] = INFINITY;
         int64_t z = -1;
         if (i < w.sq.n) {
           if (whole) {
@@ -871,7 +912,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == S::kMmaWarp) ptx::tmem_dealloc(tmem, S::kTmem);
+  if (warp == 0) ptx::tmem_dealloc(tmem, S::kTmem);
 }
 
 // Joins an item's partial results, weighted by 2^(lse_j - lse) in the order
@@ -885,24 +926,23 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(TreeArgs a) {
   const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
   const Meta m = a.meta[c];
   if (c >= m.parts || m.tile == 0) return;
-  const int begin = first_tile(m.total, m.parts, c), before = begin - first_tile(m.total, m.parts, c - 1);
+  const Stretch st(m.total, m.parts);
+  const int begin = st.begin(c), before = begin - st.begin(c - 1);
   if (m.tile > before) return;                       // an earlier CTA began it
   const int col = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const Sequence sq = sequence_of(a, m.b, false);
   const int i = (m.rt * R + col) / a.rep, h = m.rt * R + col - i * a.rep;
-  if (i >= sq.n) return;
+  if (i >= m.n) return;
   // parts: CTA c - 1 (its first or its last item), then the first items of c, c + 1, ... up to the item's end
-  const int64_t end = static_cast<int64_t>(begin) - m.tile + m.tiles;
-  int n = 2;
-  while (c + n - 1 < m.parts && first_tile(m.total, m.parts, c + n - 1) < end) ++n;
+  const int n = st.cta_of(begin - m.tile + m.tiles - 1) - c + 2;
   auto part_of = [&](int j) {
     const int64_t slot = j == 0 ? (static_cast<int64_t>(c) - 1) * 2 + (m.tile < before) : (static_cast<int64_t>(c) + j - 1) * 2;
     return slot * R + col;
   };
-  float top = -INFINITY;
+  float top = -INFINITY, near = -INFINITY;           // near: part `lane`'s
   bool nan = false;
   for (int j = lane; j < n; j += 32) {
     const float l = a.part_lse[part_of(j)];
+    if (j < 32) near = l;
     nan |= l != l;
     top = fmaxf(top, l);
   }
@@ -913,20 +953,24 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(TreeArgs a) {
 #pragma unroll
   for (int k = 0; k < E; ++k) acc[k] = 0.f;
   if (top != -INFINITY) {
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const int64_t z = part_of(j);
-      const float w = exp2f(a.part_lse[z] - top);
-      const float *p = a.part + z * D + lane * E;
-      float v[E];
-      if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
-      else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
-      total += w;
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      if (j0 > 0) near = j0 + lane < n ? a.part_lse[part_of(j0 + lane)] : -INFINITY;
+      const float weight = exp2f(near - top);
+      const int m32 = min(32, n - j0);
+#pragma unroll 8
+      for (int j = 0; j < m32; ++j) {
+        const float *p = a.part + part_of(j0 + j) * D + lane * E;
+        const float w = __shfl_sync(0xffffffffu, weight, j);
+        float v[E];
+        if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
+        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
+        total += w;
 #pragma unroll
-      for (int k = 0; k < E; ++k) acc[k] = fmaf(w, v[k], acc[k]);
+        for (int k = 0; k < E; ++k) acc[k] = fmaf(w, v[k], acc[k]);
+      }
     }
   }
-  const int64_t row = sq.first + i, head = m.g * a.rep + h;
+  const int64_t row = m.first + i, head = m.g * a.rep + h;
   const float inv = nan ? NAN : total == 0.f ? 0.f : 1.f / total;
   const int64_t at = row * a.ldot + head * a.ldoh + lane * E;
 #pragma unroll
