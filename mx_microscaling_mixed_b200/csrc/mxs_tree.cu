@@ -123,10 +123,9 @@ struct Shape {
 
 // Waits for a barrier's phase; gives up when the limit ran out or another
 // role has given up.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
   const long long t0 = clock64();
-  while (!ptx::mbar_try_wait(bar, parity)) {
+  while (!ptx::mbar_try_wait_for(bar, parity, 20000)) {
     if (*given_up) return false;
     if (clock64() - t0 > kTreeWait) {
       *given_up = 1;
@@ -135,6 +134,10 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_long(bar, parity, given_up, status);
 }
 // Among the 128 threads of a softmax warpgroup: does any of them say so?
 __device__ __forceinline__ bool any_of(int group, bool p) {
@@ -474,7 +477,8 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   using S = Shape<D, M, R, P>;
   constexpr int C = S::kCols, SK = S::kStagesK, SV = S::kStagesV;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: the compiler keeps to shared-memory instructions)
+  uint8_t *smem = smem_raw + (-ptx::smem_addr(smem_raw) & 1023u);
   // (ref: the references, negated)
   float *ref = reinterpret_cast<float *>(smem + S::kStat), *factor = ref + R, *wstat = factor + R;   // wstat[4][R]
   int64_t *place = reinterpret_cast<int64_t *>(smem + S::kPlace);
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 12);
   volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);
   int *start = reinterpret_cast<int *>(smem + S::kStart);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = ptx::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -530,17 +534,17 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     const int64_t code_pitch = a.c.code_pitch[isv], scale_pitch = a.c.scale_pitch[isv];
 
     struct Look {
-      int page, off, g;                                      // page: -2 where there is no such token
+      int page, off, g;                                      // off: -1 where there is no such token
     };
     Walk f = start_walk(a, start, R);                        // of the tile looked up last
     int ft = 0;
     auto look_up = [&]() {                                   // the page of this lane's row of the next tile
-      Look k{-2, 0, f.g};
+      Look k{0, -1, f.g};
       if (f.left <= 0) return k;
       const int p = (f.tile + ft) * kTile + w4 * 32 + lane;
       if (p < f.range.total) {
         const uint32_t pg = page_of(a, p);
-        k.page = max(a.pages[f.b * a.ldp + pg], -1);
+        k.page = a.pages[f.b * a.ldp + pg];
         k.off = static_cast<int>(p - pg * a.page_size);
       }
       if (++ft == f.count()) {
@@ -553,8 +557,8 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     auto fetch = [&](int n, const Look &k) {                 // copies of tile n, looked up before
       const uint32_t to = sbase + raw + n % kRings * S::kRaw;
       const int64_t slot = static_cast<int64_t>(k.page) * a.page_size + k.off;
-      const bool real = k.page >= 0 && slot < a.c.n_slots;
-      if (!real && k.page != -2) record_bad_index(a.status);
+      const bool real = k.off >= 0 && k.page >= 0 && slot < a.c.n_slots;
+      if (!real && k.off >= 0) record_bad_index(a.status);
       const int64_t row = real ? slot * a.c.n_kvh + k.g : 0;
       copy4(to + 32 * CR + 4 * lane, scales + row * scale_pitch, real);
       // (the lowest bit of an address says that the row is there)
@@ -579,31 +583,37 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     for (int i = 0; i < M / 4; ++i) src[i] = row_in * CR + ((blk * (M / 4) + i ^ (r8 / (8 / kChunks)) % kChunks) << 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dst[i] = (blk / 2) * kAtom + (w4 * 32 + row_in) * 128 + (((blk & 1) * 4 + i ^ r8) << 4);
+    // The products: the whole warp goes through them, so that their operands
+    // are worked out once for it, and one elected lane issues (from inside a
+    // lane's branch each product took over 100 cycles to issue).
+    const uint32_t leader = ptx::elect_one();
     auto scores = [&](int n) {                               // waits for K(n) and for the place of its scores
       bool ok = wait_phase(k_full + n % SK, (n / SK) & 1, given_up, a.status);
       if (n >= 2) ok = ok && wait_phase(p_full + (n & 1), ((n - 2) >> 1) & 1, given_up, a.status);
-      if (!ok) return false;
+      if (!__all_sync(0xffffffffu, ok)) return false;
       ptx::tc_fence_after();
-      const uint64_t kd = ptx::desc_sw128(sbase + S::kK + (n % SK) * S::kKV), qd = ptx::desc_sw128(sbase + S::kQ);
+      const uint64_t kd = ptx::desc_sw128(ptx::uniform(sbase + S::kK + (n % SK) * S::kKV)), qd = ptx::desc_sw128(sbase + S::kQ);
+      const uint32_t to = ptx::uniform(tmem + (n & 1) * R);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        ptx::mma_bf16(tmem + (n & 1) * R, kd + (((k / 4) * kAtom + (k % 4) * 32) >> 4),
-                      qd + (((k / 4) * (R * 128) + (k % 4) * 32) >> 4), S::kIdescS, k > 0);
-      ptx::mma_commit(s_done + (n & 1));
+        ptx::mma_bf16_by(leader, to, kd + (((k / 4) * kAtom + (k % 4) * 32) >> 4),
+                         qd + (((k / 4) * (R * 128) + (k % 4) * 32) >> 4), S::kIdescS, k > 0);
+      ptx::mma_commit_by(leader, s_done + (n & 1));
       return true;
     };
     auto output = [&](int n, int t) {                        // waits for V(n) and its weights
       const bool ok = wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
                       wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
-      if (!ok) return false;
+      if (!__all_sync(0xffffffffu, ok)) return false;
       ptx::tc_fence_after();
-      const bool fresh = P > 1 ? t % kPeriod == 0 : t == 0;
-      const uint64_t vd = ptx::desc_mn<64>(sbase + S::kV + (n % SV) * S::kKV, kAtom);
-      const uint64_t pd = ptx::desc_mn<S::kPWidth>(sbase + S::kP + n % S::kPBufs * S::kPBytes, S::kPAtom);
+      const uint32_t more = ptx::uniform((P > 1 ? t % kPeriod : t) != 0);
+      const uint64_t vd = ptx::desc_mn<64>(ptx::uniform(sbase + S::kV + (n % SV) * S::kKV), kAtom);
+      const uint64_t pd = ptx::desc_mn<S::kPWidth>(ptx::uniform(sbase + S::kP + n % S::kPBufs * S::kPBytes), S::kPAtom);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        ptx::mma_bf16(tmem_o, vd + k * (2048 >> 4), pd + k * (32 * S::kPWidth >> 4), S::kIdescO, !fresh || k > 0);
-      ptx::mma_commit(o_done + (n & 1));
+        ptx::mma_bf16_by(leader, ptx::uniform(tmem_o), vd + k * (2048 >> 4), pd + k * (32 * S::kPWidth >> 4), S::kIdescO,
+                         k > 0 ? 1u : more);
+      ptx::mma_commit_by(leader, o_done + (n & 1));
       return true;
     };
     Walk w = start_walk(a, start, R);
@@ -673,23 +683,20 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
         __syncwarp();                                        // (the ring's place may be written again)
         if (w4 == 0) {
           // V's second place lets its warps decode on while the weights are made: the product before this one then
-          if (lane == 0) {
-            if (!isv) ok = scores(n);
-            else if (SV == 1) ok = output(n, t);
-            else if (n > 0) ok = output(n - 1, t_before);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!isv) ok = scores(n);
+          else if (SV == 1) ok = output(n, t);
+          else if (n > 0) ok = output(n - 1, t_before);
           t_before = t;
           if (!ok) break;
         }
       }
       if (ok) w.next(a, R);
     }
-    if (w4 == 0 && lane == 0 && total > 0) {
+    if (w4 == 0 && total > 0) {
       if (ok && isv && SV > 1) ok = output(total - 1, t_before);
       if (!ok) {
-        // leave no product in flight: a last commit covers all that this thread issued
-        ptx::mma_commit(drained + isv);
+        // leave no product in flight: a last commit covers all that this lane issued
+        ptx::mma_commit_by(leader, drained + isv);
         ptx::mbar_wait_cycles(drained + isv, 0, kTreeWait);
       }
     }
@@ -716,15 +723,11 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       for (int t = 0; t < nt; ++t, ++n) {
         ok = wait_phase(s_done + (n & 1), (n >> 1) & 1, given_up, a.status);
         ptx::tc_fence_after();
-        uint32_t see = 0xFFFFFFFFu;
-        if ((w.tile + t + 1) * kTile > w.range.open) {
-          // lane k: column k's tokens of this warp, then exchanged
-          const int j0 = (w.tile + t) * kTile + w4 * 32 - w.sq.ctx;
-          const uint32_t mine = seen_tokens(a, w.sq, (row0 + col0 + lane % C) / a.rep, j0);
-          see = 0;
-#pragma unroll
-          for (int k = 0; k < C; ++k) see |= (__shfl_sync(0xffffffffu, mine, k) >> lane & 1u) << k;
-        }
+        const bool masked = (w.tile + t + 1) * kTile > w.range.open;
+        // bit lane of shfl(seen(), k): does this token's column k see it
+        auto seen = [&] {
+          return seen_tokens(a, w.sq, (row0 + col0 + lane % C) / a.rep, (w.tile + t) * kTile + w4 * 32 - w.sq.ctx);
+        };
         uint32_t s[C];
         tmem_load(tmem + lanes + (n & 1) * R + col0, s);
         float v[C], top = -INFINITY;
@@ -734,9 +737,10 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
           scale_shift(v[k], v[k + 1], s[k], s[k + 1], a.scale_log2, r.x, r.y);
           scale_shift(v[k + 2], v[k + 3], s[k + 2], s[k + 3], a.scale_log2, r.z, r.w);
         }
-        if (see != 0xFFFFFFFFu) {
+        if (masked) {
+          const uint32_t mine = seen();
 #pragma unroll
-          for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
+          for (int k = 0; k < C; ++k) v[k] = __shfl_sync(0xffffffffu, mine, k) >> lane & 1u ? v[k] : -INFINITY;
         }
 #pragma unroll
         for (int k = 0; k < C; k += 2) top = max3(top, v[k], v[k + 1]);
@@ -761,7 +765,12 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
           }
           tmem_load(tmem + lanes + (n & 1) * R + col0, s);
 #pragma unroll
-          for (int k = 0; k < C; ++k) v[k] = (see >> k) & 1u ? __uint_as_float(s[k]) * a.scale_log2 : -INFINITY;
+          for (int k = 0; k < C; ++k) v[k] = __uint_as_float(s[k]) * a.scale_log2;
+          if (masked) {
+            const uint32_t mine = seen();
+#pragma unroll
+            for (int k = 0; k < C; ++k) v[k] = __shfl_sync(0xffffffffu, mine, k) >> lane & 1u ? v[k] : -INFINITY;
+          }
           {
             float m[C];
 #pragma unroll
@@ -783,7 +792,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
 #pragma unroll
           for (int k = 0; k < C; ++k) {
             sum[k] *= factor[col0 + k];
-            v[k] = (see >> k) & 1u ? exp2_fast(v[k] + ref[col0 + k]) : 0.f;
+            v[k] = v[k] == -INFINITY ? 0.f : exp2_fast(v[k] + ref[col0 + k]);
           }
           if (t > 0) {
 #pragma unroll 1
