@@ -144,12 +144,14 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+_DT = {torch.float32: MXS_F32, torch.bfloat16: MXS_BF16}
+
+
 def _dt(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return MXS_F32
-    if t.dtype == torch.bfloat16:
-        return MXS_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    d = _DT.get(t.dtype)
+    if d is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return d
 
 
 def _rowmajor(t: torch.Tensor) -> int:
@@ -396,12 +398,12 @@ class _On:
     __slots__ = ("dev", "index", "stream", "given")
 
     def __init__(self, dev: torch.device, stream, others=()):
-        index = dev.index
         if dev.type != "cuda":
             raise ValueError("expected CUDA tensors")
         for t in others:
             if t is not None and t.device != dev:
                 raise ValueError(f"tensors on {dev} and {t.device}")
+        index = dev.index
         self.dev, self.index, self.given = dev, index, stream is not None
         if stream is None:
             self.stream = _current_stream(index)
@@ -425,6 +427,14 @@ class _On:
             return torch.empty(shape, dtype=dtype, device=self.dev)
         with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=self.dev)):
             return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def empty_like(self, t: torch.Tensor, dtype) -> torch.Tensor:
+        """The same, of t's shape (cheaper to ask for)."""
+        if not self.given:
+            if dtype is None or dtype == t.dtype:
+                return torch.empty_like(t, memory_format=torch.contiguous_format)
+            return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+        return self.empty(t.shape, dtype or t.dtype)
 
 
 # the current stream's handle by device index, without the object around it
@@ -493,12 +503,16 @@ def mxs_rope(x: torch.Tensor, pos: torch.Tensor, plan: RopePlan, *, inverse: boo
     on = _On(x.device, stream, (pos, out))
     p = _index(pos, torch.int64, T, "pos")
     if out is None:
-        out = on.empty((T, heads, d), dtype or x.dtype)
-    elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
-        raise ValueError("out: another shape or type than asked for")
-    ldot, ldoh = _heads(out, "out")
-    _check(on.call(_lib.mxs_rope, x.data_ptr(), _dt(x), T, heads, d, ldxt, ldxh, p, plan.ptr, bool(inverse),
-                   out.data_ptr(), _dt(out), ldot, ldoh, on.stream), "mxs_rope")
+        out = on.empty_like(x, dtype)
+        ldot, ldoh = heads * d, d
+    else:
+        if out.shape != x.shape or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out: another shape or type than asked for")
+        ldot, ldoh = _heads(out, "out")
+    st = on.call(_lib.mxs_rope, x.data_ptr(), _dt(x), T, heads, d, ldxt, ldxh, p, plan.ptr, bool(inverse),
+                 out.data_ptr(), _dt(out), ldot, ldoh, on.stream)
+    if st:
+        raise MxsError(st, "mxs_rope")
     return out
 
 
@@ -554,13 +568,19 @@ def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torc
     on = _On(cache.device, stream, (slot,) if out is None else (slot, *out))
     s = _index(slot, torch.int64, T, "slot")
     if out is None:
-        shape = (T, cache.n_kvh, cache.d)
-        out = on.empty(shape, dtype), on.empty(shape, dtype)
-    k, v = out
-    if k.shape != (T, cache.n_kvh, cache.d) or v.shape != k.shape or k.dtype != v.dtype:
-        raise ValueError(f"out: expected two tensors of ({T}, {cache.n_kvh}, {cache.d}) and one type")
-    _check(on.call(_lib.mxs_kv_read, cache.ptr, T, s, k.data_ptr(), *_heads(k, "k"), v.data_ptr(), *_heads(v, "v"),
-                   _dt(k), on.stream), "mxs_kv_read")
+        h, d = cache.n_kvh, cache.d
+        k = on.empty((T, h, d), dtype)
+        v = on.empty_like(k, None)
+        ldkt, ldkh = ldvt, ldvh = h * d, d
+    else:
+        k, v = out
+        if k.shape != (T, cache.n_kvh, cache.d) or v.shape != k.shape or k.dtype != v.dtype:
+            raise ValueError(f"out: expected two tensors of ({T}, {cache.n_kvh}, {cache.d}) and one type")
+        ldkt, ldkh = _heads(k, "k")
+        ldvt, ldvh = _heads(v, "v")
+    st = on.call(_lib.mxs_kv_read, cache.ptr, T, s, k.data_ptr(), ldkt, ldkh, v.data_ptr(), ldvt, ldvh, _dt(k), on.stream)
+    if st:
+        raise MxsError(st, "mxs_kv_read")
     return k, v
 
 
@@ -647,21 +667,24 @@ def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: f
     c = _tree_rows(q, batch)
     cp = ctypes.addressof(c)
     if out is None:
-        out = on.empty((rows, n_qh, d), dtype)
+        out = on.empty_like(q, dtype)
+        ldot, ldoh = n_qh * d, d
     elif out.shape != q.shape:
         raise ValueError("out: another shape than q")
+    else:
+        ldot, ldoh = _heads(out, "out")
     ot = _dt(out)
-    need = _SZ(0)
-    _check(on.call(_lib.mxs_attn_tree_workspace_bytes, cache.ptr, cp, n_qh, ot, ctypes.addressof(need)), "mxs_attn_tree")
     if workspace is None:
+        need = _SZ(0)
+        _check(on.call(_lib.mxs_attn_tree_workspace_bytes, cache.ptr, cp, n_qh, ot, ctypes.addressof(need)), "mxs_attn_tree")
         workspace = on.empty(need.value + 1024, torch.uint8)
-    elif workspace.numel() * workspace.element_size() < need.value + 255:
-        raise MxsError(9, "mxs_attn_tree")
+    ws = _aligned_ptr(workspace, 256)
+    ws_bytes = workspace.numel() * workspace.element_size() - (ws - workspace.data_ptr())
     lse = on.empty((rows, n_qh), torch.float32) if return_lse else None
-    ldot, ldoh = _heads(out, "out")
-    _check(on.call(_lib.mxs_attn_tree, q.data_ptr(), n_qh, ldqt, ldqh, cache.ptr, cp, float(sm_scale), out.data_ptr(),
-                   ot, ldot, ldoh, None if lse is None else lse.data_ptr(), _aligned_ptr(workspace, 256), need.value,
-                   on.stream), "mxs_attn_tree")
+    st = on.call(_lib.mxs_attn_tree, q.data_ptr(), n_qh, ldqt, ldqh, cache.ptr, cp, sm_scale, out.data_ptr(), ot, ldot,
+                 ldoh, None if lse is None else lse.data_ptr(), ws, max(ws_bytes, 0), on.stream)
+    if st:
+        raise MxsError(st, "mxs_attn_tree")
     return (out, lse) if return_lse else out
 
 

@@ -76,51 +76,6 @@ constexpr int kAtom = kTile * 128;               // 64 bf16 values of each token
 constexpr float kSlack = 24.f;                   // weights are kept below 2^kSlack
 constexpr long long kTreeWait = 2000000000LL;    // cycles (about 1 s)
 
-// How a CTA's shared memory is laid out for R columns (query rows), P bf16
-// pieces of a weight: what has to be there once first, then a second place
-// for what waits most, while there is room.
-template <int D, int M, int R, int P>
-struct Shape {
-  static constexpr int kSoftWarps = 8, kDecodeWarps = 8;     // two groups of four each
-  static constexpr int kThreads = (kSoftWarps + kDecodeWarps) * 32;
-  static constexpr int kCols = R / 2;                        // columns of a softmax group
-  static constexpr int kN = R * P;                           // columns of the output product
-  static constexpr int kKV = kTile * D * 2;
-  static constexpr int kPWidth = R < 64 ? R : 64;            // columns in a row of a swizzle atom of the weights
-  static constexpr int kPAtom = kTile * kPWidth * 2;
-  static constexpr int kPBytes = kTile * kN * 2;
-  static constexpr int kCodeRow = D * M / 8;                 // bytes
-  static constexpr int kRawTensor = kTile * (kCodeRow + 4);  // codes and scale words of a tile as fetched
-  static constexpr int kRaw = 2 * kRawTensor;
-  static constexpr int kQBytes = R * D * 2, kAccBytes = P > 1 ? R * D * 4 : 0;
-  static constexpr int kSmall = 6 * R * 4 + R * 8 + 16 * 8 + 256;
-  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall;
-  static constexpr int kOnce = 2 * kKV + kPBytes + kQBytes + kAccBytes + 2 * kRaw;
-  static constexpr bool kFits = kOnce <= kRoom;
-  static constexpr int kPBufs = kOnce + kPBytes <= kRoom ? 2 : 1;
-  static constexpr int kWithP = kOnce + (kPBufs - 1) * kPBytes;
-  static constexpr int kRings = kWithP + kRaw <= kRoom ? 3 : 2;          // fetched tiles
-  static constexpr int kWithRaw = kWithP + (kRings - 2) * kRaw;
-  static constexpr int kStagesK = kWithRaw + kKV <= kRoom ? 2 : 1;
-  static constexpr int kWithK = kWithRaw + (kStagesK - 1) * kKV;
-  static constexpr int kStagesV = kWithK + kKV <= kRoom ? 2 : 1;
-  static constexpr int kK = 0, kV = kStagesK * kKV, kP = kV + kStagesV * kKV, kQ = kP + kPBufs * kPBytes;
-  static constexpr int kAcc = kQ + kQBytes;                  // fp32 sums of output periods, [column][place]
-  static constexpr int kRawAt = kAcc + kAccBytes;
-  static constexpr int kStat = kRawAt + kRings * kRaw;       // per column: reference, factor, 4 maxima or sums
-  static constexpr int kPlace = kStat + 6 * R * 4;           // per column: where its output goes (64 bits)
-  static constexpr int kBar = kPlace + R * 8;
-  static constexpr int kStart = kBar + 16 * 8;               // where the CTA's work begins
-  static constexpr int kEnd = kStart + 256;
-  static constexpr int kBytes = kEnd + 1024;
-  // (heads of 64: the output product reads 64 places that nobody uses behind V's: P is there)
-  static_assert(kV + kStagesV * kKV + kAtom <= kEnd, "within the CTA's shared memory");
-  static constexpr int kTmem = 2 * R + kN <= 64 ? 64 : 2 * R + kN <= 128 ? 128 : 2 * R + kN <= 256 ? 256 : 512;
-  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTile >> 4) << 24);
-  static constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(R >> 3) << 17);
-  static constexpr uint32_t kIdescO = kIdesc | (3u << 15) | (static_cast<uint32_t>(kN >> 3) << 17);
-};
-
 // Waits for a barrier's phase; gives up when the limit ran out or another
 // role has given up.
 __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
@@ -204,22 +159,37 @@ __device__ __forceinline__ uint32_t step8(uint32_t b) { return b >= 7u ? (b - 6u
 // every intermediate is exact in bf16.  Two codes per instruction come from
 // the two halves of a word, so the values leave in the order 0 4 1 5 2 6 3 7
 // (4 bits) or 0 2 1 3 of each word (8 bits); q and the output follow it.
+// The factors of a block by its scale byte come from a table in shared
+// memory (a dozen instructions per block otherwise).
 template <int M>
 struct BlockScale {
   uint32_t s, c, s16;
-  __device__ __forceinline__ explicit BlockScale(uint32_t b) {
-    b = min(b, 249u);                            // above, -136 s leaves bf16's range
-    if constexpr (M == 4) {
-      s = step4(b) * 0x10001u;
-      c = (0x8000u | ((b + 5u) << 7) | 8u) * 0x10001u;
-      s16 = 0;
-    } else {
-      s = step8(b) * 0x10001u;
-      s16 = step4(b) * 0x10001u;
-      c = (0x8000u | ((b + 5u) << 7) | 16u) * 0x10001u;
-    }
-  }
 };
+template <>
+struct BlockScale<4> {
+  uint32_t s, c;
+};
+template <int M>
+constexpr int kTableEntry = M == 4 ? 8 : 16;
+template <int M, int THREADS>
+__device__ __forceinline__ void fill_table(uint8_t *table) {
+  for (uint32_t i = threadIdx.x; i < 256; i += THREADS) {
+    const uint32_t b = min(i, 249u);             // above, -136 s leaves bf16's range
+    const uint32_t c = (0x8000u | ((b + 5u) << 7) | (M == 4 ? 8u : 16u)) * 0x10001u;
+    if constexpr (M == 4) *reinterpret_cast<uint2 *>(table + 8 * i) = make_uint2(step4(b) * 0x10001u, c);
+    else *reinterpret_cast<uint4 *>(table + 16 * i) = make_uint4(step8(b) * 0x10001u, c, step4(b) * 0x10001u, 0);
+  }
+}
+template <int M>
+__device__ __forceinline__ BlockScale<M> block_scale(const uint8_t *table, uint32_t b) {
+  if constexpr (M == 4) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(table + 8 * b);
+    return {t.x, t.y};
+  } else {
+    const uint4 t = *reinterpret_cast<const uint4 *>(table + 16 * b);
+    return {t.x, t.y, t.z};
+  }
+}
 template <int M>
 __device__ __forceinline__ uint4 decode8(uint32_t w0, uint32_t w1, const BlockScale<M> &k) {
   uint32_t o[4];
@@ -248,6 +218,52 @@ __device__ __forceinline__ int true_position(int e) {
   if constexpr (M == 4) return (e & ~7) | ((e & 7) >> 1) | ((e & 1) << 2);
   else return (e & ~3) | ((e & 3) >> 1) | ((e & 1) << 1);
 }
+
+// How a CTA's shared memory is laid out for R columns (query rows), P bf16
+// pieces of a weight: what has to be there once first, then a second place
+// for what waits most, while there is room.
+template <int D, int M, int R, int P>
+struct Shape {
+  static constexpr int kSoftWarps = 8, kDecodeWarps = 8;     // two groups of four each
+  static constexpr int kThreads = (kSoftWarps + kDecodeWarps) * 32;
+  static constexpr int kCols = R / 2;                        // columns of a softmax group
+  static constexpr int kN = R * P;                           // columns of the output product
+  static constexpr int kKV = kTile * D * 2;
+  static constexpr int kPWidth = R < 64 ? R : 64;            // columns in a row of a swizzle atom of the weights
+  static constexpr int kPAtom = kTile * kPWidth * 2;
+  static constexpr int kPBytes = kTile * kN * 2;
+  static constexpr int kCodeRow = D * M / 8;                 // bytes
+  static constexpr int kRawTensor = kTile * (kCodeRow + 4);  // codes and scale words of a tile as fetched
+  static constexpr int kRaw = 2 * kRawTensor;
+  static constexpr int kQBytes = R * D * 2, kAccBytes = P > 1 ? R * D * 4 : 0;
+  static constexpr int kSmall = 6 * R * 4 + R * 8 + 16 * 8 + 256 + 256 * kTableEntry<M>;
+  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall;
+  static constexpr int kOnce = 2 * kKV + kPBytes + kQBytes + kAccBytes + 2 * kRaw;
+  static constexpr bool kFits = kOnce <= kRoom;
+  static constexpr int kPBufs = kOnce + kPBytes <= kRoom ? 2 : 1;
+  static constexpr int kWithP = kOnce + (kPBufs - 1) * kPBytes;
+  static constexpr int kRings = kWithP + kRaw <= kRoom ? 3 : 2;          // fetched tiles
+  static constexpr int kWithRaw = kWithP + (kRings - 2) * kRaw;
+  static constexpr int kStagesK = kWithRaw + kKV <= kRoom ? 2 : 1;
+  static constexpr int kWithK = kWithRaw + (kStagesK - 1) * kKV;
+  static constexpr int kStagesV = kWithK + kKV <= kRoom ? 2 : 1;
+  static constexpr int kK = 0, kV = kStagesK * kKV, kP = kV + kStagesV * kKV, kQ = kP + kPBufs * kPBytes;
+  static constexpr int kAcc = kQ + kQBytes;                  // fp32 sums of output periods, [column][place]
+  static constexpr int kRawAt = kAcc + kAccBytes;
+  static constexpr int kStat = kRawAt + kRings * kRaw;       // per column: reference, factor, 4 maxima or sums
+  static constexpr int kPlace = kStat + 6 * R * 4;           // per column: where its output goes (64 bits)
+  static constexpr int kBar = kPlace + R * 8;
+  static constexpr int kStart = kBar + 16 * 8;               // where the CTA's work begins
+  static constexpr int kTable = kStart + 256;                // factors by scale byte
+  static constexpr int kEnd = kTable + 256 * kTableEntry<M>;
+  static constexpr int kBytes = kEnd + 1024;
+  // (heads of 64: the output product reads 64 places that nobody uses behind V's: P is there)
+  static_assert(kV + kStagesV * kKV + kAtom <= kEnd, "within the CTA's shared memory");
+  static constexpr int kTmem = 2 * R + kN <= 64 ? 64 : 2 * R + kN <= 128 ? 128 : 2 * R + kN <= 256 ? 256 : 512;
+  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTile >> 4) << 24);
+  static constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(R >> 3) << 17);
+  static constexpr uint32_t kIdescO = kIdesc | (3u << 15) | (static_cast<uint32_t>(kN >> 3) << 17);
+};
 
 // What a row tile of a sequence covers: its rows are (drafted token i, head
 // h of the group) = (row / rep, row % rep) for rows row0 .. row0 + R - 1.
@@ -432,11 +448,14 @@ __device__ __forceinline__ Walk start_walk(const TreeArgs &a, const int *smem, i
   return w;
 }
 
+// Asynchronous copies, zeros where there is nothing real.  (Not ordered with
+// ordinary accesses by the compiler: a ring's place is handed over by
+// barriers, and the copies may go between the arithmetic of another.)
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0));
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0));
 }
 
 template <int N>
@@ -502,6 +521,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     *given_up = 0;
   }
   for (int i = threadIdx.x; i < R; i += S::kThreads) ref[i] = INFINITY;
+  fill_table<M, S::kThreads>(smem + S::kTable);
   pdl_wait();
   // tensor memory is taken after the wait for earlier kernels and before
   // later ones may start: a CTA that waits for another kernel holds none
@@ -541,24 +561,23 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     auto look_up = [&]() {                                   // the page of this lane's row of the next tile
       Look k{0, -1, f.g};
       if (f.left <= 0) return k;
-      const int p = (f.tile + ft) * kTile + w4 * 32 + lane;
-      if (p < f.range.total) {
-        const uint32_t pg = page_of(a, p);
-        k.page = a.pages[f.b * a.ldp + pg];
-        k.off = static_cast<int>(p - pg * a.page_size);
-      }
+      const int p = (f.tile + ft) * kTile + w4 * 32 + lane, real = min(p, f.range.total - 1);
+      const uint32_t pg = page_of(a, real);
+      k.page = a.pages[f.b * a.ldp + pg];
+      k.off = p == real ? static_cast<int>(p - pg * a.page_size) : -1;
       if (++ft == f.count()) {
         ft = 0;
         f.next(a, R);
       }
       return k;
     };
+    bool bad = false;
     const int in8 = lane / kChunks, swz = (in8 & 7) / (8 / kChunks) % kChunks;
     auto fetch = [&](int n, const Look &k) {                 // copies of tile n, looked up before
       const uint32_t to = sbase + raw + n % kRings * S::kRaw;
       const int64_t slot = static_cast<int64_t>(k.page) * a.page_size + k.off;
       const bool real = k.off >= 0 && k.page >= 0 && slot < a.c.n_slots;
-      if (!real && k.off >= 0) record_bad_index(a.status);
+      bad |= !real && k.off >= 0;
       const int64_t row = real ? slot * a.c.n_kvh + k.g : 0;
       copy4(to + 32 * CR + 4 * lane, scales + row * scale_pitch, real);
       // (the lowest bit of an address says that the row is there)
@@ -631,11 +650,6 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     while (ok && w.left > 0) {
       const int nt = w.count();
       for (int t = 0; t < nt; ++t, ++n) {
-        if (n + kRings - 1 < total) {
-          fetch(n + kRings - 1, next);
-          next = look_up();
-        }
-        commit();
         constexpr int kQ = R * D / 8 / 128;                  // 16-byte chunks of q per thread of K's warps
         uint4 qv[kQ];
         if (t == 0 && !isv) {
@@ -649,7 +663,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
               qv[i] = *reinterpret_cast<const uint4 *>(a.q + (w.sq.first + di) * a.ldqt + (w.g * a.rep + h) * a.ldqh + e * 8);
           }
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRings - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRings - 2) : "memory");
         __syncwarp();
         // the place of tile u is taken; for a new q, every score of the old one has to be there
         const int u = t == 0 && !isv ? n - 1 : n - (isv ? SV : SK);
@@ -664,6 +678,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
                 reorder8<M>(qv[i]);
           }
         }
+        fetch(n + kRings - 1, next);                         // (nothing behind the last tile)
         const uint8_t *from = smem + raw + n % kRings * S::kRaw;
         uint8_t *to = smem + (isv ? S::kV + n % SV * S::kKV : S::kK + n % SK * S::kKV);
 #pragma unroll
@@ -671,16 +686,18 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
           uint4 code[M / 4];
 #pragma unroll
           for (int i = 0; i < M / 4; ++i) code[i] = *reinterpret_cast<const uint4 *>(from + src[i] + it * kRows * CR);
-          const BlockScale<M> bs(from[32 * CR + 4 * row_in + blk + it * kRows * 4]);
+          const BlockScale<M> bs = block_scale<M>(smem + S::kTable, from[32 * CR + 4 * row_in + blk + it * kRows * 4]);
           const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(to + dst[j] + it * kRows * 128) =
                 decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs);
         }
+        commit();
         ptx::fence_async_shared();
         ptx::mbar_arrive(isv ? v_full + n % SV : k_full + n % SK);
         __syncwarp();                                        // (the ring's place may be written again)
+        next = look_up();
         if (w4 == 0) {
           // V's second place lets its warps decode on while the weights are made: the product before this one then
           if (!isv) ok = scores(n);
@@ -702,6 +719,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     }
     __syncwarp();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (bad) record_bad_index(a.status);
   } else {
     // -------------------------------------------------------------- softmax
     const int grp = warp >> 2, w4 = warp & 3;
