@@ -224,8 +224,9 @@ __device__ __forceinline__ int true_position(int e) {
 // for what waits most, while there is room.
 template <int D, int M, int R, int P>
 struct Shape {
-  static constexpr int kSoftWarps = 8, kDecodeWarps = 8;     // two groups of four each
-  static constexpr int kThreads = (kSoftWarps + kDecodeWarps) * 32;
+  static constexpr int kSoftWarps = 8;                       // two groups of four
+  static constexpr int kFetchWarps = R < 64 ? 8 : 4;         // for each of K and V (64 columns need the registers)
+  static constexpr int kThreads = (kSoftWarps + 2 * kFetchWarps) * 32;
   static constexpr int kCols = R / 2;                        // columns of a softmax group
   static constexpr int kN = R * P;                           // columns of the output product
   static constexpr int kKV = kTile * D * 2;
@@ -236,7 +237,7 @@ struct Shape {
   static constexpr int kRawTensor = kTile * (kCodeRow + 4);  // codes and scale words of a tile as fetched
   static constexpr int kRaw = 2 * kRawTensor;
   static constexpr int kQBytes = R * D * 2, kAccBytes = P > 1 ? R * D * 4 : 0;
-  static constexpr int kSmall = 6 * R * 4 + R * 8 + 16 * 8 + 256 + 256 * kTableEntry<M>;
+  static constexpr int kSmall = 6 * R * 4 + R * 8 + 32 * 8 + 256 + 256 * kTableEntry<M>;
   static constexpr int kRoom = 227 * 1024 - 1024 - kSmall;
   static constexpr int kOnce = 2 * kKV + kPBytes + kQBytes + kAccBytes + 2 * kRaw;
   static constexpr bool kFits = kOnce <= kRoom;
@@ -253,7 +254,7 @@ struct Shape {
   static constexpr int kStat = kRawAt + kRings * kRaw;       // per column: reference, factor, 4 maxima or sums
   static constexpr int kPlace = kStat + 6 * R * 4;           // per column: where its output goes (64 bits)
   static constexpr int kBar = kPlace + R * 8;
-  static constexpr int kStart = kBar + 16 * 8;               // where the CTA's work begins
+  static constexpr int kStart = kBar + 32 * 8;               // where the CTA's work begins
   static constexpr int kTable = kStart + 256;                // factors by scale byte
   static constexpr int kEnd = kTable + 256 * kTableEntry<M>;
   static constexpr int kBytes = kEnd + 1024;
@@ -478,10 +479,10 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 // decoded once for all of them:
 //   S^T [token][row] = K Q^T     A = K  (token x d, K-major),  B = Q
 //   O^T [d][row]    += V^T P^T   A = V  (token x d, stored along d), B = P
-// Both accumulate in tensor memory.  Eight warps fetch (asynchronous copies,
-// tiles ahead) and decode the cache into shared memory, four K and four V;
-// one lane of each issues its products; eight warps turn scores into weights,
-// four for each half of the columns.  A softmax thread owns one token and sums its
+// Both accumulate in tensor memory.  Sixteen or eight warps fetch (asynchronous
+// copies, tiles ahead) and decode the cache into shared memory, half K and
+// half V, and issue the products; eight warps turn scores into weights, four
+// for each half of the columns.  A softmax thread owns one token and sums its
 // weights per row over all tiles; the sums meet at an item's end.
 //   The running maximum of a row is a reference that weights are relative
 // to, common to all tokens: it is set by an item's first tile and moved only
@@ -502,21 +503,21 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   float *ref = reinterpret_cast<float *>(smem + S::kStat), *factor = ref + R, *wstat = factor + R;   // wstat[4][R]
   int64_t *place = reinterpret_cast<int64_t *>(smem + S::kPlace);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::kBar);
-  uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *k_full = bar + 6, *v_full = bar + 8, *drained = bar + 10;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 12);
+  uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *k_full = bar + 6, *v_full = bar + 8, *drained = bar + 12;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 10);
   volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);
   int *start = reinterpret_cast<int *>(smem + S::kStart);
   const int warp = ptx::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(k_full + i, 4 * 32);
-      ptx::mbar_init(v_full + i, 4 * 32);
+      ptx::mbar_init(k_full + i, S::kFetchWarps * 32);
+      ptx::mbar_init(v_full + i, S::kFetchWarps * 32);
       ptx::mbar_init(s_done + i, 1);
       ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
       ptx::mbar_init(o_done + i, 1);
-      ptx::mbar_init(drained + i, 1);
     }
+    for (int i = 0; i < 2 * S::kFetchWarps; ++i) ptx::mbar_init(drained + i, 1);
     ptx::fence_mbar_init();
     *given_up = 0;
   }
@@ -541,14 +542,15 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
 
   if (warp >= S::kSoftWarps) {
     // ------------------------------------------------- fetching, decoding, the products
-    // A warp has 32 rows of every tile of K or of V.  Copies of the next
-    // tiles are on their way into its own part of a ring.  The first warp of
-    // each four issues the products that take what they decode, by one lane.
+    // A warp has RW rows of every tile of K or of V.  Copies of the next
+    // tiles are on their way into its own part of a ring.  The warps take
+    // turns in issuing the products of what they decode.
+    constexpr int W = S::kFetchWarps, RW = kTile / W;
     constexpr int kRings = S::kRings;
     constexpr int CR = S::kCodeRow, kChunks = CR / 16;       // 16-byte chunks of a row
     constexpr int BL = D / kBlock;                           // blocks of a row
-    const int dw = warp - S::kSoftWarps, w4 = dw & 3, isv = dw >> 2;
-    const uint32_t raw = S::kRawAt + isv * S::kRawTensor + w4 * 32 * (CR + 4);
+    const int dw = warp - S::kSoftWarps, wt = dw % W, isv = dw / W;
+    const uint32_t raw = S::kRawAt + isv * S::kRawTensor + wt * RW * (CR + 4);
     // chunk c of row r lies at chunk c ^ (r / (8 / kChunks)) % kChunks, so that 8 rows' meet no bank conflict
     const uint8_t *codes = a.c.codes[isv], *scales = a.c.scales[isv];
     const int64_t code_pitch = a.c.code_pitch[isv], scale_pitch = a.c.scale_pitch[isv];
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     auto look_up = [&]() {                                   // the page of this lane's row of the next tile
       Look k{0, -1, f.g};
       if (f.left <= 0) return k;
-      const int p = (f.tile + ft) * kTile + w4 * 32 + lane, real = min(p, f.range.total - 1);
+      const int p = (f.tile + ft) * kTile + wt * RW + lane % RW, real = min(p, f.range.total - 1);
       const uint32_t pg = page_of(a, real);
       k.page = a.pages[f.b * a.ldp + pg];
       k.off = p == real ? static_cast<int>(p - pg * a.page_size) : -1;
@@ -579,29 +581,33 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       const bool real = k.off >= 0 && k.page >= 0 && slot < a.c.n_slots;
       bad |= !real && k.off >= 0;
       const int64_t row = real ? slot * a.c.n_kvh + k.g : 0;
-      copy4(to + 32 * CR + 4 * lane, scales + row * scale_pitch, real);
+      if (lane < RW) copy4(to + RW * CR + 4 * lane, scales + row * scale_pitch, real);
       // (the lowest bit of an address says that the row is there)
       const uint64_t addr = reinterpret_cast<uint64_t>(codes) + static_cast<uint64_t>(row * code_pitch) + real;
+      constexpr int kCopies = RW * kChunks / 32;
+      uint64_t from[kCopies];
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
+      for (int i = 0; i < kCopies; ++i) from[i] = __shfl_sync(0xffffffffu, addr, i * (32 / kChunks) + in8);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
         // rows lane / kChunks of the i-th 32 / kChunks rows, chunk lane % kChunks
         const int rr = i * (32 / kChunks) + in8, c = lane % kChunks;
         const int sw = kChunks == 8 ? ((i & 1) * 4 + in8) & 7 : swz;
-        const uint64_t from = __shfl_sync(0xffffffffu, addr, rr);
-        copy16(to + rr * CR + ((c ^ sw) << 4), reinterpret_cast<const uint8_t *>(from & ~uint64_t{1}) + 16 * c, from & 1);
+        copy16(to + rr * CR + ((c ^ sw) << 4), reinterpret_cast<const uint8_t *>(from[i] & ~uint64_t{1}) + 16 * c,
+               from[i] & 1);
       }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
     const int blk = (lane >> 3) % BL, row_in = (lane >> 3) / BL * 8 + (lane & 7);
-    constexpr int kRows = 32 / BL, kIt = BL;                 // rows per step of a warp, steps
+    constexpr int kRows = 32 / BL, kIt = RW / kRows;         // rows per step of a warp, steps
     // where this lane reads and writes: rows step by multiples of 8, the swizzles stay
     const int r8 = lane & 7;
     uint32_t src[M / 4], dst[4];
 #pragma unroll
     for (int i = 0; i < M / 4; ++i) src[i] = row_in * CR + ((blk * (M / 4) + i ^ (r8 / (8 / kChunks)) % kChunks) << 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i] = (blk / 2) * kAtom + (w4 * 32 + row_in) * 128 + (((blk & 1) * 4 + i ^ r8) << 4);
+    for (int i = 0; i < 4; ++i) dst[i] = (blk / 2) * kAtom + (wt * RW + row_in) * 128 + (((blk & 1) * 4 + i ^ r8) << 4);
     // The products: the whole warp goes through them, so that their operands
     // are worked out once for it, and one elected lane issues (from inside a
     // lane's branch each product took over 100 cycles to issue).
@@ -621,8 +627,10 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       return true;
     };
     auto output = [&](int n, int t) {                        // waits for V(n) and its weights
+      // (another warp issued the sums so far: they have to be there)
       const bool ok = wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
-                      wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
+                      wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status) &&
+                      (n == 0 || wait_phase(o_done + ((n - 1) & 1), ((n - 1) >> 1) & 1, given_up, a.status));
       if (!__all_sync(0xffffffffu, ok)) return false;
       ptx::tc_fence_after();
       const uint32_t more = ptx::uniform((P > 1 ? t % kPeriod : t) != 0);
@@ -646,20 +654,20 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     }
     Look next = ahead[kRings - 1];
     bool ok = true;
-    int n = 0, t_before = 0;
+    int n = 0;
     while (ok && w.left > 0) {
       const int nt = w.count();
       for (int t = 0; t < nt; ++t, ++n) {
-        constexpr int kQ = R * D / 8 / 128;                  // 16-byte chunks of q per thread of K's warps
+        constexpr int kQ = (R * D / 8 + W * 32 - 1) / (W * 32);  // 16-byte chunks of q per thread of K's warps
         uint4 qv[kQ];
         if (t == 0 && !isv) {
           // q of a new item: row c of the tile, zero where there is no such row
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
-            const int j = i * 128 + w4 * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+            const int j = (i * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
             const int rr = w.rt * R + c, di = rr / a.rep, h = rr - di * a.rep;
             qv[i] = make_uint4(0, 0, 0, 0);
-            if (di < w.sq.n)
+            if (di < w.sq.n && c < R)
               qv[i] = *reinterpret_cast<const uint4 *>(a.q + (w.sq.first + di) * a.ldqt + (w.g * a.rep + h) * a.ldqh + e * 8);
           }
         }
@@ -673,49 +681,50 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
         if (t == 0 && !isv) {
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
-            const int j = i * 128 + w4 * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
-            *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) =
+            const int j = (i * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+            if (c < R) *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) =
                 reorder8<M>(qv[i]);
           }
         }
         fetch(n + kRings - 1, next);                         // (nothing behind the last tile)
         const uint8_t *from = smem + raw + n % kRings * S::kRaw;
         uint8_t *to = smem + (isv ? S::kV + n % SV * S::kKV : S::kK + n % SK * S::kKV);
+        // (all loads first: the compiler may not take one past another row's stores)
+        uint4 code[kIt][M / 4];
+        uint32_t byte[kIt];
+        BlockScale<M> bs[kIt];
 #pragma unroll
         for (int it = 0; it < kIt; ++it) {
-          uint4 code[M / 4];
+          byte[it] = from[RW * CR + 4 * row_in + blk + it * kRows * 4];
 #pragma unroll
-          for (int i = 0; i < M / 4; ++i) code[i] = *reinterpret_cast<const uint4 *>(from + src[i] + it * kRows * CR);
-          const BlockScale<M> bs = block_scale<M>(smem + S::kTable, from[32 * CR + 4 * row_in + blk + it * kRows * 4]);
-          const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[0]);
+          for (int i = 0; i < M / 4; ++i) code[it][i] = *reinterpret_cast<const uint4 *>(from + src[i] + it * kRows * CR);
+        }
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) bs[it] = block_scale<M>(smem + S::kTable, byte[it]);
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[it][0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(to + dst[j] + it * kRows * 128) =
-                decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs);
+                decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs[it]);
         }
         commit();
         ptx::fence_async_shared();
         ptx::mbar_arrive(isv ? v_full + n % SV : k_full + n % SK);
         __syncwarp();                                        // (the ring's place may be written again)
         next = look_up();
-        if (w4 == 0) {
-          // V's second place lets its warps decode on while the weights are made: the product before this one then
-          if (!isv) ok = scores(n);
-          else if (SV == 1) ok = output(n, t);
-          else if (n > 0) ok = output(n - 1, t_before);
-          t_before = t;
+        if (wt == n % W) {
+          ok = isv ? output(n, t) : scores(n);
           if (!ok) break;
         }
       }
       if (ok) w.next(a, R);
     }
-    if (w4 == 0 && total > 0) {
-      if (ok && isv && SV > 1) ok = output(total - 1, t_before);
-      if (!ok) {
-        // leave no product in flight: a last commit covers all that this lane issued
-        ptx::mma_commit_by(leader, drained + isv);
-        ptx::mbar_wait_cycles(drained + isv, 0, kTreeWait);
-      }
+    if (!ok) {
+      // leave no product in flight: a last commit covers all that this lane issued
+      ptx::mma_commit_by(leader, drained + dw);
+      ptx::mbar_wait_cycles(drained + dw, 0, kTreeWait);
     }
     __syncwarp();
     asm volatile("cp.async.wait_group 0;" ::: "memory");
