@@ -1,4 +1,5 @@
-"""ctypes binding of libmxs (the C ABI in include/mxs.h), same entry-point names.
+"""Binding of libmxs (the C ABI in include/mxs.h), same entry-point names: ctypes,
+and for the ordinary form of the serving calls a small extension module.
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  torch supplies device memory (inputs, outputs, workspaces) and
@@ -15,9 +16,11 @@ from typing import List, Optional, Sequence
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxs.so")
-if not os.path.exists(_LIB_PATH):
-    raise ImportError(f"libmxs.so not built at {_LIB_PATH}; run python -m mx_microscaling_mixed_b200.build")
+for _path in (_LIB_PATH, os.path.join(os.path.dirname(_LIB_PATH), "_binding.so")):
+    if not os.path.exists(_path):
+        raise ImportError(f"{os.path.basename(_path)} not built at {_path}; run python -m mx_microscaling_mixed_b200.build")
 _lib = ctypes.CDLL(_LIB_PATH)
+from . import _binding  # noqa: E402  (the serving calls' arguments in C++; linked against libmxs.so)
 
 MXS_F32, MXS_BF16 = 0, 1
 MXS_ALLOC_FRACTIONS, MXS_ALLOC_BUDGET, MXS_ALLOC_LAYER = 0, 1, 2
@@ -454,6 +457,13 @@ def _index(t: torch.Tensor, dtype, n: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _result(r, where: str):
+    """What the extension gave: the call's results, or the status of its refusal."""
+    if isinstance(r, int):
+        raise MxsError(r, where)
+    return r
+
+
 _ROPE_KINDS = {"linear": 1, "parts": 2, "yarn": 3}
 
 
@@ -498,6 +508,10 @@ def mxs_rope(x: torch.Tensor, pos: torch.Tensor, plan: RopePlan, *, inverse: boo
     """x (tokens, heads, d; bf16 or fp32) turned to its positions pos (int64),
     as `dtype` (x's by default); out may be x.  inverse turns back: the
     gradient of x from that of the result."""
+    if out is None and stream is None:
+        r = _binding.rope(x, pos, plan.ptr, inverse, dtype)
+        if r is not None:
+            return _result(r, "mxs_rope")
     ldxt, ldxh = _heads(x, "x")
     T, heads, d = x.shape
     on = _On(x.device, stream, (pos, out))
@@ -529,6 +543,7 @@ class KVCache:
         self.device = dev[0] if dev else torch.device("cuda", torch.cuda.current_device())
         if any(x != self.device for x in dev):
             raise ValueError("K and V on different devices")
+        self.index = -1 if self.device.index is None else self.device.index
 
 
 def kv_cache_empty(n_slots: int, n_kvh: int, d: int, bits: int = 4, device="cuda") -> KVCache:
@@ -544,6 +559,10 @@ def mxs_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slot: torch.T
     """Codes the tokens k, v (tokens, n_kvh, d) into their slots (int64; a
     negative one skips the token).  With `rope` the keys are turned to pos
     (int64) first."""
+    if stream is None:
+        r = _binding.kv_write(k, v, cache.ptr, cache.index, slot, pos, None if rope is None else rope.ptr)
+        if r is not None:
+            return _check(r, "mxs_kv_write")
     ldkt, ldkh = _heads(k, "k")
     ldvt, ldvh = _heads(v, "v")
     T = k.shape[0]
@@ -564,6 +583,10 @@ def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torc
     """(k, v), each (tokens, n_kvh, d): the values in the given slots (int64).
     A negative slot leaves its rows of `out` as they are (unspecified where
     the call makes them)."""
+    if out is None and stream is None:
+        r = _binding.kv_read(cache.ptr, cache.index, slot, dtype)
+        if r is not None:
+            return _result(r, "mxs_kv_read")
     T = slot.numel()
     on = _On(cache.device, stream, (slot,) if out is None else (slot, *out))
     s = _index(slot, torch.int64, T, "slot")
@@ -586,11 +609,12 @@ def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torc
 
 class TreeBatch:
     """Drafted tokens of a batch of sequences over a paged cache."""
-    __slots__ = ("c", "ptr", "rows", "tensors", "device")
+    __slots__ = ("c", "ptr", "rows", "tensors", "device", "index")
 
     def __init__(self, c: TreeBatchC, tensors):
         self.c, self.ptr, self.tensors = c, ctypes.addressof(c), tensors
         self.rows, self.device = int(c.rows), tensors[0].device
+        self.index = -1 if self.device.index is None else self.device.index
 
 
 def tree_batch(q_start: torch.Tensor, length: torch.Tensor, pages: torch.Tensor, page_size: int, *, max_q: int,
@@ -657,6 +681,10 @@ def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: f
     (rows, n_qh, d) as `dtype` (bf16 or fp32), and with return_lse the fp32
     (rows, n_qh) logarithms of the sums.  Rows of no sequence stay as they
     are in `out` (unspecified where the call makes it)."""
+    if out is None and stream is None:
+        r = _binding.attn_tree(q, cache.ptr, cache.index, batch.ptr, batch.index, sm_scale, dtype, return_lse, workspace)
+        if r is not None:
+            return _result(r, "mxs_attn_tree")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
     ldqt, ldqh = _heads(q, "q")
