@@ -681,12 +681,12 @@ def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: f
     (rows, n_qh, d) as `dtype` (bf16 or fp32), and with return_lse the fp32
     (rows, n_qh) logarithms of the sums.  Rows of no sequence stay as they
     are in `out` (unspecified where the call makes it)."""
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bf16")
     if out is None and stream is None:
         r = _binding.attn_tree(q, cache.ptr, cache.index, batch.ptr, batch.index, sm_scale, dtype, return_lse, workspace)
         if r is not None:
             return _result(r, "mxs_attn_tree")
-    if q.dtype != torch.bfloat16:
-        raise TypeError("q must be bf16")
     ldqt, ldqh = _heads(q, "q")
     rows, n_qh, d = q.shape
     if d != cache.d:
