@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t code_of(float x, CodeScale s) {
 //   holds the k-th pairs of neighbouring units side by side, which leaves no
 //   bank conflict.  Otherwise one warp per block, one lane per position.
 template <bool F32, int M, bool VEC>
-__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, const __grid_constant__ mxs_rope_plan plan) {
+__global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a, const __grid_constant__ mxs_rope_plan plan) {
   extern __shared__ double2 turn[];
   pdl_wait();
   pdl_trigger();
@@ -78,6 +78,43 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, co
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
+    // the first unit's values of B tokens are on their way while cos and sin
+    // are evaluated
+    constexpr int B = 2;
+    const int per_head = d / 16, per_token = 2 * nh * per_head;    // K units, then V units; a multiple of 8
+    const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
+    const int sub = threadIdx.x / wide, r0 = threadIdx.x - sub * wide;
+    Raw8<F32> fv[B], fw[B];
+    int64_t fs[B];
+    struct Unit {
+      int isv, h, run0, e0, e1;
+    };
+    auto unit = [&](int r) {
+      Unit k;
+      k.isv = r >= nh * per_head;
+      const int rr = r - k.isv * nh * per_head;
+      k.h = rr / per_head;
+      const int u = rr - k.h * per_head;
+      // K in the half layout: the turned run, then the rest; else one run
+      const int split = !k.isv && a.rope && !inter ? plan.rot : 0;
+      k.run0 = u < split / 16 ? 0 : split;
+      k.e0 = k.run0 + 8 * (u - k.run0 / 16);
+      k.e1 = k.e0 + (u < split / 16 ? split : d - split) / 2;
+      return k;
+    };
+    auto fetch = [&](const Unit &k, int t) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int tb = t + b * abreast;
+        fs[b] = tb < nt ? a.slot[t0 + tb] : -1;
+        if (tb < nt) {                               // (also of a token without a slot: it is there)
+          const int64_t si = (t0 + tb) * a.ldt[k.isv] + k.h * a.ldh[k.isv];
+          fv[b] = fetch8<F32>(a.src[k.isv], si + k.e0);
+          fw[b] = fetch8<F32>(a.src[k.isv], si + k.e1);
+        }
+      }
+    };
+    if (VEC && sub < abreast) fetch(unit(r0), sub);
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kWriteThreads) {
       const int t = i / half, p = i - t * half;
@@ -86,25 +123,20 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, co
     if (threadIdx.x < nt && a.slot[t0 + threadIdx.x] >= a.c.n_slots) record_bad_index(a.status);
     __syncthreads();
     if constexpr (VEC) {
-      const int per_head = d / 16, per_token = 2 * nh * per_head;    // K units, then V units; a multiple of 8
-      const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
-      const int sub = threadIdx.x / wide;
       if (sub >= abreast) continue;
       const uint32_t four = 0xFu << (lane & ~3);         // the lanes of a block of 32 values
-      for (int r = threadIdx.x - sub * wide; r < per_token; r += wide) {
-        const int isv = r >= nh * per_head, rr = r - isv * nh * per_head;
-        const int h = rr / per_head, u = rr - h * per_head;
-        // K in the half layout: the turned run, then the rest; else one run
-        const int split = !isv && a.rope && !inter ? plan.rot : 0;
-        const int run0 = u < split / 16 ? 0 : split, n = u < split / 16 ? split : d - split;
-        const int e0 = run0 + 8 * (u - run0 / 16), e1 = e0 + n / 2;
-        for (int t = sub; t < nt; t += abreast) {
-          const int64_t slot = a.slot[t0 + t];
+      for (int r = r0; r < per_token; r += wide) {
+        const auto [isv, h, run0, e0, e1] = unit(r);
+        for (int tt = sub; tt < nt; tt += B * abreast) {
+          if (r > r0 || tt > sub) fetch(unit(r), tt);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const int t = tt + b * abreast;
+          const int64_t slot = fs[b];
           if (slot < 0 || slot >= a.c.n_slots) continue;              // all lanes of the block
           float v[8], w[8];
-          const int64_t si = (t0 + t) * a.ldt[isv] + h * a.ldh[isv];
-          load8<F32>(a.src[isv], si + e0, v);
-          load8<F32>(a.src[isv], si + e1, w);
+          widen8<F32>(fv[b], v);
+          widen8<F32>(fw[b], w);
           if (!isv && a.rope) {
             const double2 *cs = turn + t * group * groups;
             if (!inter) {
@@ -155,6 +187,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, co
             }
             if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
           }
+        }
         }
       }
     } else {

@@ -32,7 +32,7 @@ struct RopeArgs {
 // heads of 128, bf16, where the 134 MB of x and y need 20).  Otherwise a unit
 // is one pair or one copied value.
 template <bool FIN, bool FOUT, bool VEC>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ mxs_rope_plan plan) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeArgs a, const __grid_constant__ mxs_rope_plan plan) {
   extern __shared__ double2 turn[];
   pdl_wait();
   pdl_trigger();
@@ -51,6 +51,23 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a, const
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
+    // a unit's values of B tokens are on their way while cos and sin are
+    // evaluated, turned and copied units alike
+    constexpr int B = FIN ? 2 : 4;
+    Raw8<FIN> v[B], w[B];
+    auto fetch = [&](int r, int t) {
+      const int h = r / per_head, u = r - h * per_head;
+      const int e = u < turned ? u * 8 : first_copied + (u - turned) * 8;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int tb = t + b * abreast;
+        const int64_t xi = (t0 + tb) * a.ldxt + h * a.ldxh + e;
+        if (tb < nt) v[b] = fetch8<FIN>(a.x, xi);
+        if (tb < nt && u < turned && !inter) w[b] = fetch8<FIN>(a.x, xi + half);
+      }
+    };
+    const int r0 = threadIdx.x - sub * wide;
+    if (VEC && sub < abreast) fetch(r0, sub);
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
       const int t = i / half, p = i - t * half;
@@ -58,39 +75,33 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a, const
     }
     __syncthreads();
     if (sub >= abreast) continue;
-    for (int r = threadIdx.x - sub * wide; r < per_token; r += wide) {
+    for (int r = r0; r < per_token; r += wide) {
       const int h = r / per_head, u = r - h * per_head;
       const bool turns = u < turned;
       if constexpr (VEC) {
-        // all loads of B tokens first, turned and copied units alike
-        constexpr int B = 2;
         const int e = turns ? u * 8 : first_copied + (u - turned) * 8;
         const bool two = turns && !inter;
         for (int t = sub; t < nt; t += B * abreast) {
-          float v[B][8], w[B][8];
-#pragma unroll
-          for (int b = 0; b < B; ++b) {
-            const int tb = t + b * abreast;
-            const int64_t xi = (t0 + tb) * a.ldxt + h * a.ldxh + e;
-            if (tb < nt) load8<FIN>(a.x, xi, v[b]);
-            if (tb < nt && two) load8<FIN>(a.x, xi + half, w[b]);
-          }
+          if (r > r0 || t > sub) fetch(r, t);
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             const int tb = t + b * abreast;
             if (tb >= nt) break;
             const double2 *cs = turn + tb * group * turned + u;
+            const int64_t oi = (t0 + tb) * a.ldot + h * a.ldoh + e;
+            float x[8], y[8];
+            widen8<FIN>(v[b], x);
             if (two) {
+              widen8<FIN>(w[b], y);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) rope_pair(v[b][k], w[b][k], cs[k * turned]);
+              for (int k = 0; k < 8; ++k) rope_pair(x[k], y[k], cs[k * turned]);
+              store8<FOUT>(a.out, oi + half, y);
             } else if (turns) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (e / 2 + k < half) rope_pair(v[b][2 * k], v[b][2 * k + 1], cs[k * turned]);
+                if (e / 2 + k < half) rope_pair(x[2 * k], x[2 * k + 1], cs[k * turned]);
             }
-            const int64_t oi = (t0 + tb) * a.ldot + h * a.ldoh + e;
-            store8<FOUT>(a.out, oi, v[b]);
-            if (two) store8<FOUT>(a.out, oi + half, w[b]);
+            store8<FOUT>(a.out, oi, x);
           }
         }
       } else {
@@ -215,10 +226,11 @@ extern "C" mxs_status mxs_rope(const void *x, mxs_dtype xt, int64_t T, int64_t h
   a.d = static_cast<int32_t>(d);
   a.inverse = inverse != 0;
   const int sms = device_sms();
-  // four tokens a step (one where there are few), so that a step has about
-  // one cos/sin evaluation per thread
-  a.tokens = T >= 4 * sms ? std::max(1, 2 * kRopeThreads / half / 2) : 1;
-  a.tokens = std::min(a.tokens, 4);
+  // as many tokens a step as a thread has in flight, one where there are few
+  const int64_t units = heads * (vec ? (plan->layout == MXS_ROPE_HALF ? (d - half) / 8 : d / 8) : d - half);
+  const int64_t abreast = std::max<int64_t>(1, kRopeThreads / units);
+  const int64_t most = std::min<int64_t>(abreast * (xt == MXS_F32 ? 2 : 4), 2048 / std::max(half, 8));
+  a.tokens = static_cast<int32_t>(T >= 4 * sms * most ? most : std::max<int64_t>(1, std::min(most, T / (2 * sms))));
   const int64_t steps = (T + a.tokens - 1) / a.tokens;
   const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 8));
   const size_t smem = sizeof(double2) * a.tokens * ((half + 3) / 4 * 4);    // (interleaved units: whole groups of 4 pairs)

@@ -29,17 +29,32 @@ __device__ __forceinline__ float load1(const void *p, int64_t i) {
   if constexpr (F32) return static_cast<const float *>(p)[i];
   else return bf16_bits_to_float(static_cast<const uint16_t *>(p)[i]);
 }
-// 8 consecutive values from a 16-byte aligned place.
+// 8 consecutive values from a 16-byte aligned place, as they are in memory
+// (fetched early, widened late: half the registers for bf16).
 template <bool F32>
-__device__ __forceinline__ void load8(const void *p, int64_t i, float (&v)[8]) {
+struct Raw8 {
+  uint4 q[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> fetch8(const void *p, int64_t i) {
+  Raw8<F32> r;
   if constexpr (F32) {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
+    r.q[0] = s[0];
+    r.q[1] = s[1];
   } else {
-    const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    r.q[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void widen8(const Raw8<F32> &r, float (&v)[8]) {
+  if constexpr (F32) {
+    const uint32_t w[8] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w, r.q[1].x, r.q[1].y, r.q[1].z, r.q[1].w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+  } else {
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[2 * k] = __uint_as_float(w[k] << 16);
