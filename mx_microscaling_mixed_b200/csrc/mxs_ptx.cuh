@@ -106,6 +106,17 @@ __device__ __forceinline__ void mma_bf16_by(uint32_t leader, uint32_t d, uint64_
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
 }
+// The same with A in tensor memory (two 16-bit values of a row per column).
+__device__ __forceinline__ void mma_bf16_ts_by(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit_by(uint32_t leader, uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"

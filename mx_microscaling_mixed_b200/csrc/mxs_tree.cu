@@ -34,6 +34,7 @@ struct TreeArgs {
   float *lse;
   int32_t row_tiles, ctas;
   float *part, *part_lse;  // unfinished items' normalised outputs and base-2 lse: [CTA][first, last][column]([D])
+  int32_t out_vec;         // out's rows allow 16-byte stores
   Meta *meta;       // [CTA]; NULL where no item has more than one tile
   int *status;
 };
@@ -459,6 +460,135 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool real) 
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0));
 }
 
+// The fetching and decoding role of a warp: RW rows of every tile of K or of
+// V.  Copies of the next tiles are on their way into its own part of a ring.
+// `before` runs ahead of the wait for a tile's copies, `ready` waits for its
+// place in shared memory, `after` follows when the warp has handed it over;
+// the last two say whether to go on.
+template <typename S, int D, int M, int R, int W, typename Before, typename Ready, typename After>
+__device__ __forceinline__ bool fetch_tiles(const TreeArgs &a, const int *start, uint8_t *smem, int isv, int wt, int lane,
+                                            uint64_t *full, Before before, Ready ready, After after) {
+  constexpr int RW = kTile / W, kRings = S::kRings, kStages[2] = {S::kStagesK, S::kStagesV};
+  constexpr int CR = S::kCodeRow, kChunks = CR / 16;         // 16-byte chunks of a row
+  constexpr int BL = D / kBlock;                             // blocks of a row
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const int total = start[0], NS = isv ? kStages[1] : kStages[0];
+  const uint32_t raw = S::kRawAt + isv * S::kRawTensor + wt * RW * (CR + 4);
+  // chunk c of row r lies at chunk c ^ (r / (8 / kChunks)) % kChunks, so that 8 rows' meet no bank conflict
+  const uint8_t *codes = a.c.codes[isv], *scales = a.c.scales[isv];
+  const int64_t code_pitch = a.c.code_pitch[isv], scale_pitch = a.c.scale_pitch[isv];
+
+  struct Look {
+    int page, off, g;                                      // off: -1 where there is no such token
+  };
+  Walk f = start_walk(a, start, R);                        // of the tile looked up last
+  int ft = 0;
+  auto look_up = [&]() {                                   // the page of this lane's row of the next tile
+    Look k{0, -1, f.g};
+    if (f.left <= 0) return k;
+    const int p = (f.tile + ft) * kTile + wt * RW + lane % RW, real = min(p, f.range.total - 1);
+    const uint32_t pg = page_of(a, real);
+    k.page = a.pages[f.b * a.ldp + pg];
+    k.off = p == real ? static_cast<int>(p - pg * a.page_size) : -1;
+    if (++ft == f.count()) {
+      ft = 0;
+      f.next(a, R);
+    }
+    return k;
+  };
+  bool bad = false;
+  const int in8 = lane / kChunks, swz = (in8 & 7) / (8 / kChunks) % kChunks;
+  auto fetch = [&](int n, const Look &k) {                 // copies of tile n, looked up before
+    const uint32_t to = sbase + raw + n % kRings * S::kRaw;
+    const int64_t slot = static_cast<int64_t>(k.page) * a.page_size + k.off;
+    const bool real = k.off >= 0 && k.page >= 0 && slot < a.c.n_slots;
+    bad |= !real && k.off >= 0;
+    const int64_t row = real ? slot * a.c.n_kvh + k.g : 0;
+    if (lane < RW) copy4(to + RW * CR + 4 * lane, scales + row * scale_pitch, real);
+    // (the lowest bit of an address says that the row is there)
+    const uint64_t addr = reinterpret_cast<uint64_t>(codes) + static_cast<uint64_t>(row * code_pitch) + real;
+    constexpr int kCopies = RW * kChunks / 32;
+    uint64_t from[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) from[i] = __shfl_sync(0xffffffffu, addr, i * (32 / kChunks) + in8);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      // rows lane / kChunks of the i-th 32 / kChunks rows, chunk lane % kChunks
+      const int rr = i * (32 / kChunks) + in8, c = lane % kChunks;
+      const int sw = kChunks == 8 ? ((i & 1) * 4 + in8) & 7 : swz;
+      copy16(to + rr * CR + ((c ^ sw) << 4), reinterpret_cast<const uint8_t *>(from[i] & ~uint64_t{1}) + 16 * c,
+             from[i] & 1);
+    }
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+  const int blk = (lane >> 3) % BL, row_in = (lane >> 3) / BL * 8 + (lane & 7);
+  constexpr int kRows = 32 / BL, kIt = RW / kRows;         // rows per step of a warp, steps
+  // where this lane reads and writes: rows step by multiples of 8, the swizzles stay
+  const int r8 = lane & 7;
+  uint32_t src[M / 4], dst[4];
+#pragma unroll
+  for (int i = 0; i < M / 4; ++i) src[i] = row_in * CR + ((blk * (M / 4) + i ^ (r8 / (8 / kChunks)) % kChunks) << 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dst[i] = (blk / 2) * kAtom + (wt * RW + row_in) * 128 + (((blk & 1) * 4 + i ^ r8) << 4);
+  Walk w = start_walk(a, start, R);
+  Look ahead[kRings];
+#pragma unroll
+  for (int n = 0; n < kRings; ++n) ahead[n] = look_up();
+#pragma unroll
+  for (int n = 0; n < kRings - 1; ++n) {
+    if (n < total) fetch(n, ahead[n]);
+    commit();
+  }
+  Look next = ahead[kRings - 1];
+  bool ok = true;
+  int n = 0;
+  while (ok && w.left > 0) {
+    const int nt = w.count();
+    for (int t = 0; t < nt; ++t, ++n) {
+      before(w, t);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRings - 2) : "memory");
+      __syncwarp();
+      ok = ready(w, t, n);
+      if (!ok) break;
+      fetch(n + kRings - 1, next);                         // (nothing behind the last tile)
+      const uint8_t *from = smem + raw + n % kRings * S::kRaw;
+      uint8_t *to = smem + (isv ? S::kV : S::kK) + n % NS * S::kKV;
+      // (all loads first: the compiler may not take one past another row's stores)
+      uint4 code[kIt][M / 4];
+      uint32_t byte[kIt];
+      BlockScale<M> bs[kIt];
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        byte[it] = from[RW * CR + 4 * row_in + blk + it * kRows * 4];
+#pragma unroll
+        for (int i = 0; i < M / 4; ++i) code[it][i] = *reinterpret_cast<const uint4 *>(from + src[i] + it * kRows * CR);
+      }
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) bs[it] = block_scale<M>(smem + S::kTable, byte[it]);
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[it][0]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4 *>(to + dst[j] + it * kRows * 128) =
+              decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs[it]);
+      }
+      commit();
+      ptx::fence_async_shared();
+      ptx::mbar_arrive(full + n % NS);
+      __syncwarp();                                        // (the ring's place may be written again)
+      next = look_up();
+      ok = after(n, t);
+      if (!ok) break;
+    }
+    if (ok) w.next(a, R);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (bad) record_bad_index(a.status);
+  return ok;
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 8) {
@@ -538,76 +668,12 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_o = tmem + 2 * R;
   const uint32_t sbase = ptx::smem_addr(smem);
-  const int total = start[0];                        // the CTA's tiles; n counts them
 
   if (warp >= S::kSoftWarps) {
     // ------------------------------------------------- fetching, decoding, the products
-    // A warp has RW rows of every tile of K or of V.  Copies of the next
-    // tiles are on their way into its own part of a ring.  The warps take
-    // turns in issuing the products of what they decode.
-    constexpr int W = S::kFetchWarps, RW = kTile / W;
-    constexpr int kRings = S::kRings;
-    constexpr int CR = S::kCodeRow, kChunks = CR / 16;       // 16-byte chunks of a row
-    constexpr int BL = D / kBlock;                           // blocks of a row
+    // The warps take turns in issuing the products of what they decode.
+    constexpr int W = S::kFetchWarps;
     const int dw = warp - S::kSoftWarps, wt = dw % W, isv = dw / W;
-    const uint32_t raw = S::kRawAt + isv * S::kRawTensor + wt * RW * (CR + 4);
-    // chunk c of row r lies at chunk c ^ (r / (8 / kChunks)) % kChunks, so that 8 rows' meet no bank conflict
-    const uint8_t *codes = a.c.codes[isv], *scales = a.c.scales[isv];
-    const int64_t code_pitch = a.c.code_pitch[isv], scale_pitch = a.c.scale_pitch[isv];
-
-    struct Look {
-      int page, off, g;                                      // off: -1 where there is no such token
-    };
-    Walk f = start_walk(a, start, R);                        // of the tile looked up last
-    int ft = 0;
-    auto look_up = [&]() {                                   // the page of this lane's row of the next tile
-      Look k{0, -1, f.g};
-      if (f.left <= 0) return k;
-      const int p = (f.tile + ft) * kTile + wt * RW + lane % RW, real = min(p, f.range.total - 1);
-      const uint32_t pg = page_of(a, real);
-      k.page = a.pages[f.b * a.ldp + pg];
-      k.off = p == real ? static_cast<int>(p - pg * a.page_size) : -1;
-      if (++ft == f.count()) {
-        ft = 0;
-        f.next(a, R);
-      }
-      return k;
-    };
-    bool bad = false;
-    const int in8 = lane / kChunks, swz = (in8 & 7) / (8 / kChunks) % kChunks;
-    auto fetch = [&](int n, const Look &k) {                 // copies of tile n, looked up before
-      const uint32_t to = sbase + raw + n % kRings * S::kRaw;
-      const int64_t slot = static_cast<int64_t>(k.page) * a.page_size + k.off;
-      const bool real = k.off >= 0 && k.page >= 0 && slot < a.c.n_slots;
-      bad |= !real && k.off >= 0;
-      const int64_t row = real ? slot * a.c.n_kvh + k.g : 0;
-      if (lane < RW) copy4(to + RW * CR + 4 * lane, scales + row * scale_pitch, real);
-      // (the lowest bit of an address says that the row is there)
-      const uint64_t addr = reinterpret_cast<uint64_t>(codes) + static_cast<uint64_t>(row * code_pitch) + real;
-      constexpr int kCopies = RW * kChunks / 32;
-      uint64_t from[kCopies];
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) from[i] = __shfl_sync(0xffffffffu, addr, i * (32 / kChunks) + in8);
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        // rows lane / kChunks of the i-th 32 / kChunks rows, chunk lane % kChunks
-        const int rr = i * (32 / kChunks) + in8, c = lane % kChunks;
-        const int sw = kChunks == 8 ? ((i & 1) * 4 + in8) & 7 : swz;
-        copy16(to + rr * CR + ((c ^ sw) << 4), reinterpret_cast<const uint8_t *>(from[i] & ~uint64_t{1}) + 16 * c,
-               from[i] & 1);
-      }
-    };
-    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-
-    const int blk = (lane >> 3) % BL, row_in = (lane >> 3) / BL * 8 + (lane & 7);
-    constexpr int kRows = 32 / BL, kIt = RW / kRows;         // rows per step of a warp, steps
-    // where this lane reads and writes: rows step by multiples of 8, the swizzles stay
-    const int r8 = lane & 7;
-    uint32_t src[M / 4], dst[4];
-#pragma unroll
-    for (int i = 0; i < M / 4; ++i) src[i] = row_in * CR + ((blk * (M / 4) + i ^ (r8 / (8 / kChunks)) % kChunks) << 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i] = (blk / 2) * kAtom + (wt * RW + row_in) * 128 + (((blk & 1) * 4 + i ^ r8) << 4);
     // The products: the whole warp goes through them, so that their operands
     // are worked out once for it, and one elected lane issues (from inside a
     // lane's branch each product took over 100 cycles to issue).
@@ -643,92 +709,44 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       ptx::mma_commit_by(leader, o_done + (n & 1));
       return true;
     };
-    Walk w = start_walk(a, start, R);
-    Look ahead[kRings];
+    constexpr int kQ = (R * D / 8 + W * 32 - 1) / (W * 32);  // 16-byte chunks of q per thread of K's warps
+    uint4 qv[kQ];
+    auto before = [&](const Walk &w, int t) {
+      if (t > 0 || isv) return;
+      // q of a new item: row c of the tile, zero where there is no such row
 #pragma unroll
-    for (int n = 0; n < kRings; ++n) ahead[n] = look_up();
+      for (int i = 0; i < kQ; ++i) {
+        const int j = (i * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+        const int rr = w.rt * R + c, di = rr / a.rep, h = rr - di * a.rep;
+        qv[i] = make_uint4(0, 0, 0, 0);
+        if (di < w.sq.n && c < R)
+          qv[i] = *reinterpret_cast<const uint4 *>(a.q + (w.sq.first + di) * a.ldqt + (w.g * a.rep + h) * a.ldqh + e * 8);
+      }
+    };
+    auto ready = [&](const Walk &, int t, int n) {
+      // the place of tile u is taken; for a new q, every score of the old one has to be there
+      const int u = t == 0 && !isv ? n - 1 : n - (isv ? SV : SK);
+      bool ok = true;
+      if (u >= 0) ok = wait_phase((isv ? o_done : s_done) + (u & 1), (u >> 1) & 1, given_up, a.status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (t == 0 && !isv) {
 #pragma unroll
-    for (int n = 0; n < kRings - 1; ++n) {
-      if (n < total) fetch(n, ahead[n]);
-      commit();
-    }
-    Look next = ahead[kRings - 1];
-    bool ok = true;
-    int n = 0;
-    while (ok && w.left > 0) {
-      const int nt = w.count();
-      for (int t = 0; t < nt; ++t, ++n) {
-        constexpr int kQ = (R * D / 8 + W * 32 - 1) / (W * 32);  // 16-byte chunks of q per thread of K's warps
-        uint4 qv[kQ];
-        if (t == 0 && !isv) {
-          // q of a new item: row c of the tile, zero where there is no such row
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) {
-            const int j = (i * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
-            const int rr = w.rt * R + c, di = rr / a.rep, h = rr - di * a.rep;
-            qv[i] = make_uint4(0, 0, 0, 0);
-            if (di < w.sq.n && c < R)
-              qv[i] = *reinterpret_cast<const uint4 *>(a.q + (w.sq.first + di) * a.ldqt + (w.g * a.rep + h) * a.ldqh + e * 8);
-          }
-        }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRings - 2) : "memory");
-        __syncwarp();
-        // the place of tile u is taken; for a new q, every score of the old one has to be there
-        const int u = t == 0 && !isv ? n - 1 : n - (isv ? SV : SK);
-        if (u >= 0) ok = wait_phase((isv ? o_done : s_done) + (u & 1), (u >> 1) & 1, given_up, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (t == 0 && !isv) {
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) {
-            const int j = (i * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
-            if (c < R) *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) =
+        for (int i = 0; i < kQ; ++i) {
+          const int j = (i * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+          if (c < R)
+            *reinterpret_cast<uint4 *>(smem + S::kQ + (e / 8) * (R * 128) + c * 128 + (((e & 7) ^ (c & 7)) << 4)) =
                 reorder8<M>(qv[i]);
-          }
-        }
-        fetch(n + kRings - 1, next);                         // (nothing behind the last tile)
-        const uint8_t *from = smem + raw + n % kRings * S::kRaw;
-        uint8_t *to = smem + (isv ? S::kV + n % SV * S::kKV : S::kK + n % SK * S::kKV);
-        // (all loads first: the compiler may not take one past another row's stores)
-        uint4 code[kIt][M / 4];
-        uint32_t byte[kIt];
-        BlockScale<M> bs[kIt];
-#pragma unroll
-        for (int it = 0; it < kIt; ++it) {
-          byte[it] = from[RW * CR + 4 * row_in + blk + it * kRows * 4];
-#pragma unroll
-          for (int i = 0; i < M / 4; ++i) code[it][i] = *reinterpret_cast<const uint4 *>(from + src[i] + it * kRows * CR);
-        }
-#pragma unroll
-        for (int it = 0; it < kIt; ++it) bs[it] = block_scale<M>(smem + S::kTable, byte[it]);
-#pragma unroll
-        for (int it = 0; it < kIt; ++it) {
-          const uint32_t *wd = reinterpret_cast<const uint32_t *>(&code[it][0]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(to + dst[j] + it * kRows * 128) =
-                decode8<M>(wd[j * M / 4], M == 8 ? wd[j * M / 4 + 1] : 0, bs[it]);
-        }
-        commit();
-        ptx::fence_async_shared();
-        ptx::mbar_arrive(isv ? v_full + n % SV : k_full + n % SK);
-        __syncwarp();                                        // (the ring's place may be written again)
-        next = look_up();
-        if (wt == n % W) {
-          ok = isv ? output(n, t) : scores(n);
-          if (!ok) break;
         }
       }
-      if (ok) w.next(a, R);
-    }
-    if (!ok) {
+      return true;
+    };
+    auto after = [&](int n, int t) { return wt != n % W ? true : isv ? output(n, t) : scores(n); };
+    if (!fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready, after)) {
       // leave no product in flight: a last commit covers all that this lane issued
       ptx::mma_commit_by(leader, drained + dw);
       ptx::mbar_wait_cycles(drained + dw, 0, kTreeWait);
     }
     __syncwarp();
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (bad) record_bad_index(a.status);
   } else {
     // -------------------------------------------------------------- softmax
     const int grp = warp >> 2, w4 = warp & 3;
@@ -951,6 +969,318 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   if (warp == 0) ptx::tmem_dealloc(tmem, S::kTmem);
 }
 
+// Shared memory of tree_rows_kernel, filled like Shape.
+template <int D, int M>
+struct RowsShape {
+  static constexpr int kSoftWarps = 8, kFetchWarps = 8, kMmaWarp = kSoftWarps + 2 * kFetchWarps;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kKV = kTile * D * 2;
+  static constexpr int kCodeRow = D * M / 8;
+  static constexpr int kRawTensor = kTile * (kCodeRow + 4);
+  static constexpr int kRaw = 2 * kRawTensor;
+  static constexpr int kQHalf = 128 * D * 2;                 // 128 rows of q
+  static constexpr int kSmall = 16 * 8 + 256 + 256 * kTableEntry<M>;
+  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall;
+  static constexpr int kOnce = 2 * kKV + 2 * kQHalf + 2 * kRaw;
+  static constexpr int kRings = kOnce + kRaw <= kRoom ? 3 : 2;
+  static constexpr int kWithRaw = kOnce + (kRings - 2) * kRaw;
+  static constexpr int kStagesK = kWithRaw + kKV <= kRoom ? 2 : 1;
+  static constexpr int kWithK = kWithRaw + (kStagesK - 1) * kKV;
+  static constexpr int kStagesV = kWithK + kKV <= kRoom ? 2 : 1;
+  static constexpr int kK = 0, kV = kStagesK * kKV, kQ = kV + kStagesV * kKV;
+  static constexpr int kRawAt = kQ + 2 * kQHalf;
+  static constexpr int kBar = kRawAt + kRings * kRaw;
+  static constexpr int kStart = kBar + 16 * 8;
+  static constexpr int kTable = kStart + 256;
+  static constexpr int kBytes = kTable + 256 * kTableEntry<M> + 1024;
+  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(128 >> 4) << 24);
+  static constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(kTile >> 3) << 17);
+  static constexpr uint32_t kIdescO = kIdesc | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
+  static constexpr int kTmemO = 2 * kTile, kTmem = 512;
+};
+
+// The same for many rows: query rows are the matrix instruction's rows, twice
+// 128 of them per CTA, so that a cache tile is decoded once for 256 rows and
+// the products run at full width:
+//   S [row][token] = Q K^T       A = Q  (row x d, K-major),     B = K
+//   O [row][d]    += P V         A = P  (tensor memory, in S's place), B = V
+// The two halves take turns: while one's scores become weights the other's
+// products run.  A softmax thread owns a row: its maximum, its sum and its
+// output's lane in tensor memory need no one else.  The maximum that weights
+// are relative to moves when a score passes it by more than 2^kSlack.
+template <int D, int M>
+__global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel(TreeArgs a) {
+  using S = RowsShape<D, M>;
+  constexpr int R = 256, SK = S::kStagesK, SV = S::kStagesV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + (-ptx::smem_addr(smem_raw) & 1023u);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::kBar);
+  uint64_t *s_done = bar, *p_full = bar + 2, *o_done = bar + 4, *k_full = bar + 6, *v_full = bar + 8, *k_free = bar + 10,
+           *v_free = bar + 12, *drained = bar + 14;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 15);
+  volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);
+  int *start = reinterpret_cast<int *>(smem + S::kStart);
+  const int warp = ptx::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(s_done + i, 1);
+      ptx::mbar_init(p_full + i, 128);
+      ptx::mbar_init(o_done + i, 1);
+      ptx::mbar_init(k_full + i, S::kFetchWarps * 32);
+      ptx::mbar_init(v_full + i, S::kFetchWarps * 32);
+      ptx::mbar_init(k_free + i, 1);
+      ptx::mbar_init(v_free + i, 1);
+    }
+    ptx::mbar_init(drained, 1);
+    ptx::fence_mbar_init();
+    *given_up = 0;
+  }
+  fill_table<M, S::kThreads>(smem + S::kTable);
+  pdl_wait();
+  if (warp == S::kMmaWarp) {
+    ptx::tmem_alloc(tmem_slot, S::kTmem);
+    ptx::tmem_relinquish();
+  }
+  find_work<R, S::kThreads>(a, start);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const int total = start[0];
+  // halves of an item that have rows
+  auto halves = [&](const Walk &w) { return w.sq.n * a.rep - w.rt * R > 128 ? 2 : 1; };
+
+  if (warp == S::kMmaWarp) {
+    // ------------------------------------------------------ matrix products
+    const uint32_t leader = ptx::elect_one();
+    bool ok = true;
+    auto await = [&](uint64_t *b, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && wait_phase(b, parity, given_up, a.status));
+      ptx::tc_fence_after();
+      return ok;
+    };
+    auto scores = [&](int n, int q) {
+      const uint64_t qd = ptx::desc_sw128(ptx::uniform(sbase + S::kQ + q * S::kQHalf));
+      const uint64_t kd = ptx::desc_sw128(ptx::uniform(sbase + S::kK + n % SK * S::kKV));
+      const uint32_t to = ptx::uniform(tmem + q * kTile);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t step = ((k / 4) * kAtom + (k % 4) * 32) >> 4;
+        ptx::mma_bf16_by(leader, to, qd + step, kd + step, S::kIdescS, k > 0);
+      }
+      ptx::mma_commit_by(leader, s_done + q);
+    };
+    auto output = [&](int n, int q, uint32_t more) {
+      const uint64_t vd = ptx::desc_mn<64>(ptx::uniform(sbase + S::kV + n % SV * S::kKV), kAtom);
+      const uint32_t from = ptx::uniform(tmem + q * kTile), to = ptx::uniform(tmem + S::kTmemO + q * D);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        ptx::mma_bf16_ts_by(leader, to, from + k * 8, vd + k * (2048 >> 4), S::kIdescO, k > 0 ? 1u : more);
+      ptx::mma_commit_by(leader, o_done + q);
+    };
+    Walk w = start_walk(a, start, R);
+    int n = 0, done[2] = {0, 0};                     // tiles so far, of each half
+    if (total > 0 && await(k_full, 0)) {
+      const int nq = halves(w);
+      for (int q = 0; q < nq; ++q) scores(0, q);
+      ptx::mma_commit_by(leader, k_free);
+    }
+    while (ok && w.left > 0) {
+      const int nt = w.count(), nq = halves(w);
+      Walk after = w;
+      after.next(a, R);
+      for (int t = 0; t < nt && ok; ++t, ++n) {
+        const int nq2 = t + 1 < nt ? nq : after.left > 0 ? halves(after) : 0;
+        await(v_full + n % SV, (n / SV) & 1);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (q < nq && ok && await(p_full + q, done[q] & 1)) {
+            ++done[q];
+            output(n, q, t > 0);
+            if (q == nq - 1) ptx::mma_commit_by(leader, v_free + n % SV);
+          }
+          // (the next scores of this half go where its weights were: behind their product, in order)
+          if (q < nq2 && ok && (q > 0 || await(k_full + (n + 1) % SK, ((n + 1) / SK) & 1))) {
+            scores(n + 1, q);
+            if (q == nq2 - 1) ptx::mma_commit_by(leader, k_free + (n + 1) % SK);
+          }
+        }
+      }
+      w = after;
+    }
+    if (!ok) {
+      ptx::mma_commit_by(leader, drained);
+      ptx::mbar_wait_cycles(drained, 0, kTreeWait);
+    }
+    __syncwarp();
+  } else if (warp >= S::kSoftWarps) {
+    // ------------------------------------------------- fetching and decoding
+    constexpr int W = S::kFetchWarps;
+    const int dw = warp - S::kSoftWarps, wt = dw % W, isv = dw / W;
+    auto before = [](const Walk &, int) {};
+    auto ready = [&](const Walk &w, int t, int n) {
+      bool ok = true;
+      if (isv) {
+        if (n >= SV) ok = wait_phase(v_free + n % SV, ((n - SV) / SV) & 1, given_up, a.status);
+        return __all_sync(0xffffffffu, ok) != 0;
+      }
+      const int u = t == 0 ? n - 1 : n - SK;
+      if (u >= 0) ok = wait_phase(k_free + u % SK, (u / SK) & 1, given_up, a.status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (t == 0) {
+        // q of a new item, zero where there is no such row; negated for a negative scale
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+        constexpr int B = 4, kQ = R * D / 8 / (W * 32);
+#pragma unroll 1
+        for (int i0 = 0; i0 < kQ; i0 += B) {
+          uint4 v[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const int j = ((i0 + i) * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+            const int rr = w.rt * R + c, di = rr / a.rep, h = rr - di * a.rep;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (di < w.sq.n)
+              v[i] = *reinterpret_cast<const uint4 *>(a.q + (w.sq.first + di) * a.ldqt + (w.g * a.rep + h) * a.ldqh + e * 8);
+          }
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const int j = ((i0 + i) * W + wt) * 32 + lane, c = j / (D / 8), e = j - c * (D / 8);
+            v[i] = reorder8<M>(v[i]);
+            *reinterpret_cast<uint4 *>(smem + S::kQ + (c / 128) * S::kQHalf + (e / 8) * kAtom + (c % 128) * 128 +
+                                       (((e & 7) ^ (c & 7)) << 4)) =
+                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+          }
+        }
+      }
+      return true;
+    };
+    auto after = [](int, int) { return true; };
+    fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready, after);
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int q = warp >> 2, tok = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tmem_s = tmem + lanes + q * kTile, tmem_o = tmem + lanes + S::kTmemO + q * D;
+    const float scale = fabsf(a.scale_log2);
+    Walk w = start_walk(a, start, R);
+    bool ok = true, first = true;
+    int done = 0;                                    // tiles of this half
+    for (; ok && w.left > 0; first = false, w.next(a, R)) {
+      if (q >= halves(w)) continue;
+      const int nt = w.count(), rr = w.rt * R + q * 128 + tok, i = rr / a.rep, h = rr - i * a.rep;
+      float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+      for (int t = 0; t < nt; ++t, ++done) {
+        ok = wait_phase(s_done + q, done & 1, given_up, a.status);
+        if (done > 0) ok = ok && wait_phase(o_done + q, (done - 1) & 1, given_up, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const bool masked = (w.tile + t + 1) * kTile > w.range.open;
+        const int j0 = (w.tile + t) * kTile - w.sq.ctx;
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t s[32];
+          tmem_load(tmem_s + c, s);
+          if (masked) {
+            const uint32_t see = seen_tokens(a, w.sq, i, j0 + c);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] : 0xFF800000u;
+          }
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+        }
+        top = top == -INFINITY ? top : top * scale;
+        const bool up = top > m + kSlack || (m == -INFINITY && top != m);
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? exp2f(m - top) : 1.f;
+          l0 *= f;
+          l1 *= f;
+          if (up) m = top;
+          if (t > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_load(tmem_o + c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              ptx::tmem_st16(tmem_o + c, o);
+            }
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t s[32];
+          tmem_load(tmem_s + c, s);
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) scale_shift(v[k], v[k + 1], s[k], s[k + 1], scale, shift, shift);
+          if (masked) {
+            const uint32_t see = seen_tokens(a, w.sq, i, j0 + c);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = (see >> k) & 1u ? v[k] : -INFINITY;
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            v[2 * k] = exp2_fast(v[2 * k]);
+            v[2 * k + 1] = exp2_fast(v[2 * k + 1]);
+            add2(l0, l1, v[2 * k], v[2 * k + 1]);
+            p[k] = pack2(v[2 * k], v[2 * k + 1]);
+          }
+          ptx::tmem_st16(tmem_s + c / 2, p);         // (over scores that have been read)
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full + q);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, wait_phase(o_done + q, (done - 1) & 1, given_up, a.status));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float l = l0 + l1, inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+      const bool whole = w.whole(), has = i < w.sq.n;
+      const int64_t row = w.sq.first + i, head = w.g * a.rep + h;
+      // a CTA has at most two unfinished items, its first and its last
+      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + !first) * R + q * 128 + tok;
+      if (has && whole && a.lse) a.lse[row * a.n_qh + head] = lse2 * kLn2;
+      if (has && !whole) a.part_lse[slot] = lse2;
+      uint16_t *out = static_cast<uint16_t *>(a.out) + row * a.ldot + head * a.ldoh;
+      float *part = a.part + slot * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        tmem_load(tmem_o + c, o);
+        if (!has) continue;
+#pragma unroll
+        for (int g8 = 0; g8 < 16; g8 += 8) {
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float z = __uint_as_float(o[g8 + k]);
+            y[true_position<M>(k)] = inv == 0.f ? 0.f : z * inv;
+          }
+          if (!whole) store8<true>(part, c + g8, y);
+          else if (a.out_vec) store8<false>(out, c + g8, y);
+          else
+#pragma unroll
+            for (int k = 0; k < 8; ++k) store1<false>(out, c + g8 + k, y[k]);
+        }
+      }
+      ptx::tc_fence_before();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == S::kMmaWarp) ptx::tmem_dealloc(tmem, S::kTmem);
+}
+
 // Joins an item's partial results, weighted by 2^(lse_j - lse) in the order
 // of the CTAs.  Block (c, chunk of 8 columns) takes the item that CTA c found
 // begun by the CTA before it, if that was the item's first; one warp a column.
@@ -1071,8 +1401,9 @@ Cut tree_cut(const TreeArgs &a, bool fout, int sms) {
   Cut c{};
   c.pieces = fout ? 3 : 1;
   const int64_t group_rows = static_cast<int64_t>(a.max_q) * a.rep;
+  // (bf16 outputs of more rows: tree_rows_kernel, 256 rows of its own kind)
   const int most = fout && a.c.d == 128 && a.c.bits == 8 ? 32 : 64;
-  c.R = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : most;
+  c.R = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : group_rows <= 64 || fout ? most : 256;
   c.row_tiles = (group_rows + c.R - 1) / c.R;
   const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(a.max_len) + kTile - 1) / kTile);
   const __int128 all = static_cast<__int128>(tiles) * c.row_tiles * a.c.n_kvh * a.B;
@@ -1101,8 +1432,22 @@ mxs_status launch_tree(const TreeArgs &a, cudaStream_t s) {
   return cuda_status(cudaGetLastError());
 }
 template <int D, int M>
+mxs_status launch_rows(const TreeArgs &a, cudaStream_t s) {
+  using S = RowsShape<D, M>;
+  static_assert(S::kOnce <= S::kRoom && S::kBytes <= 227 * 1024, "a CTA's shared memory");
+  if (!ensure_smem(tree_rows_kernel<D, M>, S::kBytes)) return MXS_ERR_CUDA;
+  launch_pdl(tree_rows_kernel<D, M>, dim3(static_cast<unsigned>(a.ctas)), dim3(S::kThreads), S::kBytes, s, a);
+  count_launch();
+  if (a.meta && a.ctas > 1) {
+    launch_pdl(tree_combine_kernel<D, 256, false>, dim3(static_cast<unsigned>(a.ctas - 1), 256 / 8), dim3(256), 0, s, a);
+    count_launch();
+  }
+  return cuda_status(cudaGetLastError());
+}
+template <int D, int M>
 mxs_status launch_shape(const TreeArgs &a, const Cut &c, cudaStream_t s) {
   if (c.pieces == 1) {
+    if (c.R == 256) return launch_rows<D, M>(a, s);
     if (c.R == 16) return launch_tree<D, M, 16, 1, false>(a, s);
     if (c.R == 32) return launch_tree<D, M, 32, 1, false>(a, s);
     return launch_tree<D, M, 64, 1, false>(a, s);
@@ -1161,6 +1506,7 @@ extern "C" mxs_status mxs_attn_tree(const void *q, int64_t n_qh, int64_t ldqt, i
   a.out = out;
   a.ldot = ldot;
   a.ldoh = ldoh;
+  a.out_vec = aligned16(out) && ldot % 8 == 0 && ldoh % 8 == 0;
   a.lse = lse;
   a.row_tiles = static_cast<int32_t>(c.row_tiles);
   a.ctas = static_cast<int32_t>(c.ctas);
