@@ -109,6 +109,20 @@ __device__ __forceinline__ bool any_of(int group, bool p) {
 __device__ __forceinline__ void group_sync(int group) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
 }
+// The same for the 256 softmax threads of a half in tree_rows_kernel.
+__device__ __forceinline__ bool any_of256(int half, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(half + 1)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void half_sync(int half) {
+  asm volatile("barrier.cta.sync %0, 256;" ::"r"(half + 1) : "memory");
+}
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -972,14 +986,14 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
 // Shared memory of tree_rows_kernel, filled like Shape.
 template <int D, int M>
 struct RowsShape {
-  static constexpr int kSoftWarps = 8, kFetchWarps = 8, kMmaWarp = kSoftWarps + 2 * kFetchWarps;
+  static constexpr int kSoftWarps = 16, kFetchWarps = 4, kMmaWarp = kSoftWarps + 2 * kFetchWarps;
   static constexpr int kThreads = (kMmaWarp + 1) * 32;
   static constexpr int kKV = kTile * D * 2;
   static constexpr int kCodeRow = D * M / 8;
   static constexpr int kRawTensor = kTile * (kCodeRow + 4);
   static constexpr int kRaw = 2 * kRawTensor;
   static constexpr int kQHalf = 128 * D * 2;                 // 128 rows of q
-  static constexpr int kSmall = 16 * 8 + 256 + 256 * kTableEntry<M>;
+  static constexpr int kSmall = 16 * 8 + 256 + 256 * kTableEntry<M> + 512 * 4;
   static constexpr int kRoom = 227 * 1024 - 1024 - kSmall;
   static constexpr int kOnce = 2 * kKV + 2 * kQHalf + 2 * kRaw;
   static constexpr int kRings = kOnce + kRaw <= kRoom ? 3 : 2;
@@ -992,7 +1006,8 @@ struct RowsShape {
   static constexpr int kBar = kRawAt + kRings * kRaw;
   static constexpr int kStart = kBar + 16 * 8;
   static constexpr int kTable = kStart + 256;
-  static constexpr int kBytes = kTable + 256 * kTableEntry<M> + 1024;
+  static constexpr int kSwap = kTable + 256 * kTableEntry<M>;    // a maximum or sum of each softmax thread
+  static constexpr int kBytes = kSwap + 512 * 4 + 1024;
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(128 >> 4) << 24);
   static constexpr uint32_t kIdescS = kIdesc | (static_cast<uint32_t>(kTile >> 3) << 17);
   static constexpr uint32_t kIdescO = kIdesc | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
@@ -1005,9 +1020,11 @@ struct RowsShape {
 //   S [row][token] = Q K^T       A = Q  (row x d, K-major),     B = K
 //   O [row][d]    += P V         A = P  (tensor memory, in S's place), B = V
 // The two halves take turns: while one's scores become weights the other's
-// products run.  A softmax thread owns a row: its maximum, its sum and its
-// output's lane in tensor memory need no one else.  The maximum that weights
-// are relative to moves when a score passes it by more than 2^kSlack.
+// products run.  Two softmax threads share a row, 64 tokens of a tile and half
+// of its output each (one thread with all 128 took 329 us where two take less:
+// a half's products wait for its weights, so their latency counts).  The
+// maximum that weights are relative to moves, by a vote of the half, when a
+// score passes it by more than 2^kSlack.
 template <int D, int M>
 __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel(TreeArgs a) {
   using S = RowsShape<D, M>;
@@ -1025,7 +1042,7 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(s_done + i, 1);
-      ptx::mbar_init(p_full + i, 128);
+      ptx::mbar_init(p_full + i, 256);
       ptx::mbar_init(o_done + i, 1);
       ptx::mbar_init(k_full + i, S::kFetchWarps * 32);
       ptx::mbar_init(v_full + i, S::kFetchWarps * 32);
@@ -1078,7 +1095,7 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
       const uint32_t from = ptx::uniform(tmem + q * kTile), to = ptx::uniform(tmem + S::kTmemO + q * D);
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        ptx::mma_bf16_ts_by(leader, to, from + k * 8, vd + k * (2048 >> 4), S::kIdescO, k > 0 ? 1u : more);
+        ptx::mma_bf16_ts_by(leader, to, from + (k / 4) * 64 + (k % 4) * 8, vd + k * (2048 >> 4), S::kIdescO, k > 0 ? 1u : more);
       ptx::mma_commit_by(leader, o_done + q);
     };
     Walk w = start_walk(a, start, R);
@@ -1161,9 +1178,12 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
     fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready, after);
   } else {
     // -------------------------------------------------------------- softmax
-    const int q = warp >> 2, tok = (warp & 3) * 32 + lane;
+    const int q = warp >> 3, part = (warp >> 2) & 1, tok = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tmem_s = tmem + lanes + q * kTile, tmem_o = tmem + lanes + S::kTmemO + q * D;
+    // this thread's 64 scores, with its weights in their first 32 columns, and its half of the output
+    const uint32_t tmem_s = tmem + lanes + q * kTile + part * 64, tmem_o = tmem + lanes + S::kTmemO + q * D + part * (D / 2);
+    float *mine = reinterpret_cast<float *>(smem + S::kSwap) + (warp >> 2) * 128 + tok;
+    const float *other = reinterpret_cast<float *>(smem + S::kSwap) + ((warp >> 2) ^ 1) * 128 + tok;
     const float scale = fabsf(a.scale_log2);
     Walk w = start_walk(a, start, R);
     bool ok = true, first = true;
@@ -1174,15 +1194,13 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
       float m = -INFINITY, l0 = 0.f, l1 = 0.f;
       for (int t = 0; t < nt; ++t, ++done) {
         ok = wait_phase(s_done + q, done & 1, given_up, a.status);
-        if (done > 0) ok = ok && wait_phase(o_done + q, (done - 1) & 1, given_up, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (done > 0) ok = wait_phase(o_done + q, (done - 1) & 1, given_up, a.status) && ok;
         ptx::tc_fence_after();
         const bool masked = (w.tile + t + 1) * kTile > w.range.open;
-        const int j0 = (w.tile + t) * kTile - w.sq.ctx;
+        const int j0 = (w.tile + t) * kTile + part * 64 - w.sq.ctx;
         float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t s[32];
           tmem_load(tmem_s + c, s);
           if (masked) {
@@ -1194,26 +1212,36 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
           for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
         }
         top = top == -INFINITY ? top : top * scale;
-        const bool up = top > m + kSlack || (m == -INFINITY && top != m);
-        if (__any_sync(0xffffffffu, up)) {
-          const float f = up ? exp2f(m - top) : 1.f;
-          l0 *= f;
-          l1 *= f;
-          if (up) m = top;
-          if (t > 0) {
+        // (the vote also carries a wait that ran out: all of the half leave together)
+        if (any_of256(q, top > m + kSlack || (m == -INFINITY && top != m) || !ok)) {
+          *mine = ok ? top : NAN;
+          half_sync(q);
+          const float both = fmaxf(top, *other);
+          if (any_of256(q, !ok)) {
+            ok = false;
+            break;
+          }
+          const bool up = both > m + kSlack || (m == -INFINITY && both != m);
+          if (__any_sync(0xffffffffu, up)) {
+            const float f = up ? exp2f(m - both) : 1.f;
+            l0 *= f;
+            l1 *= f;
+            if (up) m = both;
+            if (t > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tmem_load(tmem_o + c, o);
+              for (int c = 0; c < D / 2; c += 16) {
+                uint32_t o[16];
+                tmem_load(tmem_o + c, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              ptx::tmem_st16(tmem_o + c, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                ptx::tmem_st16(tmem_o + c, o);
+              }
             }
           }
         }
         const float shift = m == -INFINITY ? 0.f : -m;
 #pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t s[32];
           tmem_load(tmem_s + c, s);
           float v[32];
@@ -1239,21 +1267,23 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
         ptx::mbar_arrive(p_full + q);
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, wait_phase(o_done + q, (done - 1) & 1, given_up, a.status));
-      if (!ok) break;
+      *mine = l0 + l1;
+      ok = wait_phase(o_done + q, (done - 1) & 1, given_up, a.status);
+      if (any_of256(q, !ok)) break;
       ptx::tc_fence_after();
-      const float l = l0 + l1, inv = l == 0.f ? 0.f : 1.f / l;
+      // (the same order in both threads)
+      const float l = part ? *other + (l0 + l1) : (l0 + l1) + *other, inv = l == 0.f ? 0.f : 1.f / l;
       const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
       const bool whole = w.whole(), has = i < w.sq.n;
       const int64_t row = w.sq.first + i, head = w.g * a.rep + h;
       // a CTA has at most two unfinished items, its first and its last
       const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + !first) * R + q * 128 + tok;
-      if (has && whole && a.lse) a.lse[row * a.n_qh + head] = lse2 * kLn2;
-      if (has && !whole) a.part_lse[slot] = lse2;
-      uint16_t *out = static_cast<uint16_t *>(a.out) + row * a.ldot + head * a.ldoh;
-      float *part = a.part + slot * D;
+      if (has && whole && a.lse && !part) a.lse[row * a.n_qh + head] = lse2 * kLn2;
+      if (has && !whole && !part) a.part_lse[slot] = lse2;
+      uint16_t *out = static_cast<uint16_t *>(a.out) + row * a.ldot + head * a.ldoh + part * (D / 2);
+      float *left = a.part + slot * D + part * (D / 2);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int c = 0; c < D / 2; c += 16) {
         uint32_t o[16];
         tmem_load(tmem_o + c, o);
         if (!has) continue;
@@ -1265,13 +1295,14 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
             const float z = __uint_as_float(o[g8 + k]);
             y[true_position<M>(k)] = inv == 0.f ? 0.f : z * inv;
           }
-          if (!whole) store8<true>(part, c + g8, y);
+          if (!whole) store8<true>(left, c + g8, y);
           else if (a.out_vec) store8<false>(out, c + g8, y);
           else
 #pragma unroll
             for (int k = 0; k < 8; ++k) store1<false>(out, c + g8 + k, y[k]);
         }
       }
+      half_sync(q);                                  // (the sums have been read)
       ptx::tc_fence_before();
     }
   }
