@@ -998,9 +998,9 @@ struct RowsShape {
   static constexpr int kOnce = 2 * kKV + 2 * kQHalf + 2 * kRaw;
   static constexpr int kRings = kOnce + kRaw <= kRoom ? 3 : 2;
   static constexpr int kWithRaw = kOnce + (kRings - 2) * kRaw;
-  static constexpr int kStagesK = kWithRaw + kKV <= kRoom ? 2 : 1;
-  static constexpr int kWithK = kWithRaw + (kStagesK - 1) * kKV;
-  static constexpr int kStagesV = kWithK + kKV <= kRoom ? 2 : 1;
+  static constexpr int kStagesV = kWithRaw + kKV <= kRoom ? 2 : 1;     // (V is waited for first)
+  static constexpr int kWithV = kWithRaw + (kStagesV - 1) * kKV;
+  static constexpr int kStagesK = kWithV + kKV <= kRoom ? 2 : 1;
   static constexpr int kK = 0, kV = kStagesK * kKV, kQ = kV + kStagesV * kKV;
   static constexpr int kRawAt = kQ + 2 * kQHalf;
   static constexpr int kBar = kRawAt + kRings * kRaw;
