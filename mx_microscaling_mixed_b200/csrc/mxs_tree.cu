@@ -79,7 +79,7 @@ constexpr long long kTreeWait = 2000000000LL;    // cycles (about 1 s)
 
 // Waits for a barrier's phase; gives up when the limit ran out or another
 // role has given up.
-__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait_for(bar, parity, 20000)) {
     if (*given_up) return false;
@@ -241,7 +241,10 @@ template <int D, int M, int R, int P>
 struct Shape {
   static constexpr int kSoftWarps = 8;                       // two groups of four
   static constexpr int kFetchWarps = R < 64 ? 8 : 4;         // for each of K and V (64 columns need the registers)
-  static constexpr int kThreads = (kSoftWarps + 2 * kFetchWarps) * 32;
+  static constexpr int kMmaWarp = kSoftWarps + 2 * kFetchWarps;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  // 64 columns: the softmax warps need 120 registers; 96 a thread at the launch, 256 x (120 - 96) = 256 x (96 - 72) moved
+  static constexpr bool kMoveRegisters = R == 64;
   static constexpr int kCols = R / 2;                        // columns of a softmax group
   static constexpr int kN = R * P;                           // columns of the output product
   static constexpr int kKV = kTile * D * 2;
@@ -258,11 +261,11 @@ struct Shape {
   static constexpr bool kFits = kOnce <= kRoom;
   static constexpr int kPBufs = kOnce + kPBytes <= kRoom ? 2 : 1;
   static constexpr int kWithP = kOnce + (kPBufs - 1) * kPBytes;
-  static constexpr int kRings = kWithP + kRaw <= kRoom ? 3 : 2;          // fetched tiles
-  static constexpr int kWithRaw = kWithP + (kRings - 2) * kRaw;
-  static constexpr int kStagesK = kWithRaw + kKV <= kRoom ? 2 : 1;
-  static constexpr int kWithK = kWithRaw + (kStagesK - 1) * kKV;
-  static constexpr int kStagesV = kWithK + kKV <= kRoom ? 2 : 1;
+  static constexpr int kStagesV = kWithP + kKV <= kRoom ? 2 : 1;
+  static constexpr int kWithV = kWithP + (kStagesV - 1) * kKV;
+  static constexpr int kStagesK = kWithV + kKV <= kRoom ? 2 : 1;
+  static constexpr int kWithK = kWithV + (kStagesK - 1) * kKV;
+  static constexpr int kRings = kWithK + kRaw <= kRoom ? 3 : 2;          // fetched tiles
   static constexpr int kK = 0, kV = kStagesK * kKV, kP = kV + kStagesV * kKV, kQ = kP + kPBufs * kPBytes;
   static constexpr int kAcc = kQ + kQBytes;                  // fp32 sums of output periods, [column][place]
   static constexpr int kRawAt = kAcc + kAccBytes;
@@ -477,11 +480,10 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool real) 
 // The fetching and decoding role of a warp: RW rows of every tile of K or of
 // V.  Copies of the next tiles are on their way into its own part of a ring.
 // `before` runs ahead of the wait for a tile's copies, `ready` waits for its
-// place in shared memory, `after` follows when the warp has handed it over;
-// the last two say whether to go on.
-template <typename S, int D, int M, int R, int W, typename Before, typename Ready, typename After>
-__device__ __forceinline__ bool fetch_tiles(const TreeArgs &a, const int *start, uint8_t *smem, int isv, int wt, int lane,
-                                            uint64_t *full, Before before, Ready ready, After after) {
+// place in shared memory and says whether to go on.
+template <typename S, int D, int M, int R, int W, typename Before, typename Ready>
+__device__ __forceinline__ void fetch_tiles(const TreeArgs &a, const int *start, uint8_t *smem, int isv, int wt, int lane,
+                                            uint64_t *full, Before before, Ready ready) {
   constexpr int RW = kTile / W, kRings = S::kRings, kStages[2] = {S::kStagesK, S::kStagesV};
   constexpr int CR = S::kCodeRow, kChunks = CR / 16;         // 16-byte chunks of a row
   constexpr int BL = D / kBlock;                             // blocks of a row
@@ -593,14 +595,11 @@ __device__ __forceinline__ bool fetch_tiles(const TreeArgs &a, const int *start,
       ptx::mbar_arrive(full + n % NS);
       __syncwarp();                                        // (the ring's place may be written again)
       next = look_up();
-      ok = after(n, t);
-      if (!ok) break;
     }
     if (ok) w.next(a, R);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (bad) record_bad_index(a.status);
-  return ok;
 }
 
 template <int N>
@@ -625,7 +624,7 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 //   O^T [d][row]    += V^T P^T   A = V  (token x d, stored along d), B = P
 // Both accumulate in tensor memory.  Sixteen or eight warps fetch (asynchronous
 // copies, tiles ahead) and decode the cache into shared memory, half K and
-// half V, and issue the products; eight warps turn scores into weights, four
+// half V; one warp issues the products; eight warps turn scores into weights, four
 // for each half of the columns.  A softmax thread owns one token and sums its
 // weights per row over all tiles; the sums meet at an item's end.
 //   The running maximum of a row is a reference that weights are relative
@@ -661,7 +660,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
       ptx::mbar_init(o_done + i, 1);
     }
-    for (int i = 0; i < 2 * S::kFetchWarps; ++i) ptx::mbar_init(drained + i, 1);
+    ptx::mbar_init(drained, 1);
     ptx::fence_mbar_init();
     *given_up = 0;
   }
@@ -683,19 +682,14 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
   const uint32_t tmem_o = tmem + 2 * R;
   const uint32_t sbase = ptx::smem_addr(smem);
 
-  if (warp >= S::kSoftWarps) {
-    // ------------------------------------------------- fetching, decoding, the products
-    // The warps take turns in issuing the products of what they decode.
-    constexpr int W = S::kFetchWarps;
-    const int dw = warp - S::kSoftWarps, wt = dw % W, isv = dw / W;
-    // The products: the whole warp goes through them, so that their operands
-    // are worked out once for it, and one elected lane issues (from inside a
-    // lane's branch each product took over 100 cycles to issue).
+  if (warp == S::kMmaWarp) {
+    // ------------------------------------------------------ matrix products
+    // The whole warp goes through them, so that their operands are worked out
+    // once for it, and one elected lane issues (from inside a lane's branch
+    // each product took over 100 cycles to issue).
     const uint32_t leader = ptx::elect_one();
-    auto scores = [&](int n) {                               // waits for K(n) and for the place of its scores
-      bool ok = wait_phase(k_full + n % SK, (n / SK) & 1, given_up, a.status);
-      if (n >= 2) ok = ok && wait_phase(p_full + (n & 1), ((n - 2) >> 1) & 1, given_up, a.status);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+    auto scores = [&](int n) {                               // waits for K(n); the place of its scores is free
+      if (!__all_sync(0xffffffffu, wait_phase(k_full + n % SK, (n / SK) & 1, given_up, a.status))) return false;
       ptx::tc_fence_after();
       const uint64_t kd = ptx::desc_sw128(ptx::uniform(sbase + S::kK + (n % SK) * S::kKV)), qd = ptx::desc_sw128(sbase + S::kQ);
       const uint32_t to = ptx::uniform(tmem + (n & 1) * R);
@@ -706,23 +700,40 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       ptx::mma_commit_by(leader, s_done + (n & 1));
       return true;
     };
-    auto output = [&](int n, int t) {                        // waits for V(n) and its weights
-      // (another warp issued the sums so far: they have to be there)
-      const bool ok = wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
-                      wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status) &&
-                      (n == 0 || wait_phase(o_done + ((n - 1) & 1), ((n - 1) >> 1) & 1, given_up, a.status));
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      ptx::tc_fence_after();
-      const uint32_t more = ptx::uniform((P > 1 ? t % kPeriod : t) != 0);
-      const uint64_t vd = ptx::desc_mn<64>(ptx::uniform(sbase + S::kV + (n % SV) * S::kKV), kAtom);
-      const uint64_t pd = ptx::desc_mn<S::kPWidth>(ptx::uniform(sbase + S::kP + n % S::kPBufs * S::kPBytes), S::kPAtom);
+    Walk w = start_walk(a, start, R);
+    const int total = start[0];
+    bool ok = total == 0 || scores(0);
+    for (int n = 0; ok && w.left > 0; w.next(a, R)) {
+      const int nt = w.count();
+      for (int t = 0; t < nt && ok; ++t, ++n) {
+        // (the scores of n + 1 go where those of n - 1 were: their weights have been waited for)
+        if (n + 1 < total) ok = scores(n + 1);
+        ok = ok && wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
+             wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t more = ptx::uniform((P > 1 ? t % kPeriod : t) != 0);
+        const uint64_t vd = ptx::desc_mn<64>(ptx::uniform(sbase + S::kV + (n % SV) * S::kKV), kAtom);
+        const uint64_t pd = ptx::desc_mn<S::kPWidth>(ptx::uniform(sbase + S::kP + n % S::kPBufs * S::kPBytes), S::kPAtom);
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        ptx::mma_bf16_by(leader, ptx::uniform(tmem_o), vd + k * (2048 >> 4), pd + k * (32 * S::kPWidth >> 4), S::kIdescO,
-                         k > 0 ? 1u : more);
-      ptx::mma_commit_by(leader, o_done + (n & 1));
-      return true;
-    };
+        for (int k = 0; k < kTile / 16; ++k)
+          ptx::mma_bf16_by(leader, ptx::uniform(tmem_o), vd + k * (2048 >> 4), pd + k * (32 * S::kPWidth >> 4), S::kIdescO,
+                           k > 0 ? 1u : more);
+        ptx::mma_commit_by(leader, o_done + (n & 1));
+      }
+    }
+    if (!ok) {
+      // leave no product in flight: a last commit covers all that were issued
+      ptx::mma_commit_by(leader, drained);
+      ptx::mbar_wait_cycles(drained, 0, kTreeWait);
+    }
+    __syncwarp();
+  } else if (warp >= S::kSoftWarps) {
+    // ------------------------------------------------- fetching and decoding
+    constexpr int W = S::kFetchWarps;
+    const int dw = warp - S::kSoftWarps, wt = dw % W, isv = dw / W;
+    if constexpr (S::kMoveRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     constexpr int kQ = (R * D / 8 + W * 32 - 1) / (W * 32);  // 16-byte chunks of q per thread of K's warps
     uint4 qv[kQ];
     auto before = [&](const Walk &w, int t) {
@@ -754,15 +765,10 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
       }
       return true;
     };
-    auto after = [&](int n, int t) { return wt != n % W ? true : isv ? output(n, t) : scores(n); };
-    if (!fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready, after)) {
-      // leave no product in flight: a last commit covers all that this lane issued
-      ptx::mma_commit_by(leader, drained + dw);
-      ptx::mbar_wait_cycles(drained + dw, 0, kTreeWait);
-    }
-    __syncwarp();
+    fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready);
   } else {
     // -------------------------------------------------------------- softmax
+    if constexpr (S::kMoveRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     const int grp = warp >> 2, w4 = warp & 3;
     const int tok = w4 * 32 + lane, col0 = grp * C;
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
@@ -1174,8 +1180,7 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
       }
       return true;
     };
-    auto after = [](int, int) { return true; };
-    fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready, after);
+    fetch_tiles<S, D, M, R, W>(a, start, smem, isv, wt, lane, isv ? v_full : k_full, before, ready);
   } else {
     // -------------------------------------------------------------- softmax
     const int q = warp >> 3, part = (warp >> 2) & 1, tok = (warp & 3) * 32 + lane;
