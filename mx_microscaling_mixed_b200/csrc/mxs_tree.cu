@@ -95,6 +95,12 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
   if (ptx::mbar_try_wait(bar, parity)) return true;
   return wait_long(bar, parity, given_up, status);
 }
+// One arrival for a warp whose lanes have each made their writes visible:
+// arrivals of single lanes on one barrier go through one after the other.
+__device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(bar);
+}
 // Among the 128 threads of a softmax warpgroup: does any of them say so?
 __device__ __forceinline__ bool any_of(int group, bool p) {
   uint32_t r;
@@ -592,8 +598,7 @@ __device__ __forceinline__ void fetch_tiles(const TreeArgs &a, const int *start,
       }
       commit();
       ptx::fence_async_shared();
-      ptx::mbar_arrive(full + n % NS);
-      __syncwarp();                                        // (the ring's place may be written again)
+      arrive_warp(full + n % NS, lane);                      // (and the ring's place may be written again)
       next = look_up();
     }
     if (ok) w.next(a, R);
@@ -654,10 +659,10 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(k_full + i, S::kFetchWarps * 32);
-      ptx::mbar_init(v_full + i, S::kFetchWarps * 32);
+      ptx::mbar_init(k_full + i, S::kFetchWarps);
+      ptx::mbar_init(v_full + i, S::kFetchWarps);
       ptx::mbar_init(s_done + i, 1);
-      ptx::mbar_init(p_full + i, S::kSoftWarps * 32);
+      ptx::mbar_init(p_full + i, S::kSoftWarps);
       ptx::mbar_init(o_done + i, 1);
     }
     ptx::mbar_init(drained, 1);
@@ -915,7 +920,7 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
         }
         ptx::fence_async_shared();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(p_full + (n & 1));
+        arrive_warp(p_full + (n & 1), lane);
       }
       if (!ok) break;
       // the sums over the tokens: lanes, then warps, in a fixed order
@@ -1048,10 +1053,10 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(s_done + i, 1);
-      ptx::mbar_init(p_full + i, 256);
+      ptx::mbar_init(p_full + i, 8);
       ptx::mbar_init(o_done + i, 1);
-      ptx::mbar_init(k_full + i, S::kFetchWarps * 32);
-      ptx::mbar_init(v_full + i, S::kFetchWarps * 32);
+      ptx::mbar_init(k_full + i, S::kFetchWarps);
+      ptx::mbar_init(v_full + i, S::kFetchWarps);
       ptx::mbar_init(k_free + i, 1);
       ptx::mbar_init(v_free + i, 1);
     }
@@ -1269,7 +1274,7 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(p_full + q);
+        arrive_warp(p_full + q, lane);
       }
       if (!ok) break;
       *mine = l0 + l1;
