@@ -246,7 +246,7 @@ __device__ __forceinline__ int true_position(int e) {
 template <int D, int M, int R, int P>
 struct Shape {
   static constexpr int kSoftWarps = 8;                       // two groups of four
-  static constexpr int kFetchWarps = R < 64 ? 8 : 4;         // for each of K and V (64 columns need the registers)
+  static constexpr int kFetchWarps = 4;                      // for each of K and V (with eight: 178 us where four took 141)
   static constexpr int kMmaWarp = kSoftWarps + 2 * kFetchWarps;
   static constexpr int kThreads = (kMmaWarp + 1) * 32;
   // 64 columns: the softmax warps need 120 registers; 96 a thread at the launch, 256 x (120 - 96) = 256 x (96 - 72) moved
