@@ -410,7 +410,7 @@ def test_bad_batches_are_left_out_and_recorded(c):
         out = run(True)
         assert torch.equal(out[:2], want[:2]) and torch.all(out[2:] == 5.0)
     q_start[2] = 4
-    for bad in (-1, 1 << 20, (1 << 31) - 1):                      # a page outside the pool: its tokens are seen by none
+    for bad in (-1, 1 << 20, (1 << 31) - 1):                      # a page outside the pool: keys and values of zero
         keep = pages[1, 0].item()
         pages[1, 0] = bad
         out = run(True)
@@ -443,6 +443,140 @@ def test_strides_streams_and_repeats(c):
     b = c.mxs_attn_tree(q, cache, batch, 0.1)
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want)
+
+
+MORE = [
+    # ctx, counts, n_qh, n_kvh, d, bits, page, causal
+    ([2500, 40], [17, 3], 16, 2, 128, 4, 16, False),              # 136 rows: half of the wide form's second half
+    ([1500], [40], 32, 4, 64, 8, 33, True),                       # 320 rows: a second row tile with one half
+    ([4100], [5], 12, 4, 128, 8, 64, False),                      # 16 columns over 33 tiles
+    ([3000, 2900, 10], [9, 10, 1], 6, 2, 64, 4, 7, True),         # 32 columns, parts of items at both ends of a CTA
+    ([2600], [20], 6, 2, 128, 8, 128, False),                     # 64 rows of 8 bits
+]
+
+
+@pytest.mark.parametrize("shape", MORE, ids=[str(i) for i in range(len(MORE))])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("sm", [0.11, -0.07])
+def test_long_items_and_both_signs_of_the_scale(c, shape, bf16, sm):
+    *shape, causal = shape
+    q, cache, batch, (qs, ctx, pages, page), mask = _case(c, *shape, causal, seed=sum(shape[0]) + shape[4])
+    out, lse = c.mxs_attn_tree(q, cache, batch, sm, dtype=torch.bfloat16 if bf16 else torch.float32, return_lse=True)
+    c.mxs_sync()
+    # a negative scale is that of the negated query
+    _check(c, out, lse, q if sm > 0 else -q, cache, qs, ctx, pages, page, abs(sm), mask, bf16)
+
+
+@pytest.mark.parametrize("n_qh", [2, 12, 40])                    # 16 and 64 columns, the wide form
+def test_scores_that_rise_over_many_tiles(c, n_qh):
+    """The reference of the weights moves again and again, and output periods
+    end between."""
+    n_slots, d, n = 4096, 64, 5
+    cache = c.kv_cache_empty(n_slots, 1, d, 8)
+    k = torch.zeros(n_slots, 1, d, device="cuda")
+    k[:, 0, 0] = torch.arange(n_slots, device="cuda") * 0.25
+    c.mxs_kv_write(k, _randn(n_slots, 1, d, seed=18), cache, torch.arange(n_slots, device="cuda"))
+    q = torch.zeros(n, n_qh, d, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 0] = (torch.arange(n * n_qh, device="cuda").view(n, n_qh) % 7 - 3.0) * 0.5
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = c.tree_batch(torch.tensor([0, n], **i32), torch.tensor([n_slots - n], **i32), torch.zeros(1, 1, **i32), n_slots,
+                         max_q=n, max_len=n_slots)
+    for dt in (torch.bfloat16, torch.float32):
+        out, lse = c.mxs_attn_tree(q, cache, batch, 1.0, dtype=dt, return_lse=True)
+        _check(c, out, lse, q, cache, np.array([0, n]), [n_slots - n], [[0]], n_slots, 1.0, None, dt == torch.bfloat16)
+
+
+def test_many_small_sequences(c):
+    """More items than CTAs, most of them within one tile, empty ones between."""
+    rng = np.random.default_rng(90)
+    ctx = [int(x) for x in rng.integers(0, 200, 301)]
+    counts = [int(x) for x in rng.integers(0, 4, 301)]
+    q, cache, batch, where, mask = _case(c, ctx, counts, 4, 2, 64, 4, 16, True, seed=91)
+    for dt in (torch.bfloat16, torch.float32):
+        out, lse = c.mxs_attn_tree(q, cache, batch, 0.2, dtype=dt, return_lse=True)
+        _check(c, out, lse, q, cache, *where, 0.2, None, dt == torch.bfloat16)
+    # one call of the whole batch is what calls of its sequences give
+    i32 = dict(dtype=torch.int32, device="cuda")
+    qs, _, pages, page = where
+    for b in (0, 150, 300):
+        if counts[b] == 0:
+            continue
+        one = c.tree_batch(torch.tensor([0, counts[b]], **i32), torch.tensor([ctx[b]], **i32),
+                           torch.tensor(pages[b: b + 1], **i32), page, max_q=counts[b], max_len=ctx[b] + counts[b])
+        alone = c.mxs_attn_tree(q[qs[b]: qs[b + 1]], cache, one, 0.2, dtype=torch.float32)
+        assert (alone - out[qs[b]: qs[b + 1]]).abs().max() <= 1e-5
+
+
+def test_forms_of_a_call_agree(c):
+    """What the extension marshals and what the general path does: given
+    outputs, streams and types, outputs that allow no vector stores."""
+    for counts, n_qh in (([8, 8], 8), ([40, 3], 32)):             # the second: the wide form
+        q, cache, batch, _, _ = _case(c, [500, 260], counts, n_qh, 2, 128, 4, 16, False, seed=17)
+        rows = q.shape[0]
+        for dt in (torch.bfloat16, torch.float32):
+            want, wl = c.mxs_attn_tree(q, cache, batch, 0.1, dtype=dt, return_lse=True)
+            odd = torch.full((rows, n_qh * 128 + 3), 7.0, dtype=dt, device="cuda")
+            out = odd[:, 1: 1 + n_qh * 128].unflatten(1, (n_qh, 128))
+            got, gl = c.mxs_attn_tree(q, cache, batch, 0.1, out=out, return_lse=True)
+            assert torch.equal(got, want) and torch.equal(gl, wl)
+            assert torch.all(odd[:, 0] == 7.0) and torch.all(odd[:, -2:] == 7.0)
+            got = c.mxs_attn_tree(q, cache, batch, 0.1, dtype=dt, stream=torch.cuda.current_stream())
+            assert torch.equal(got, want)
+    x, pos, plan = _randn(5, 3, 128, seed=1), torch.arange(5, device="cuda"), c.mxs_rope_plan(128)
+    for dt in (None, torch.bfloat16):
+        want = c.mxs_rope(x, pos, plan, dtype=dt)
+        assert torch.equal(c.mxs_rope(x, pos, plan, out=torch.empty_like(want)), want)
+        assert torch.equal(c.mxs_rope(x, pos, plan, dtype=dt, stream=torch.cuda.current_stream()), want)
+    small = c.kv_cache_empty(5, 3, 128, 8)
+    c.mxs_kv_write(x, x, small, pos, pos=pos, rope=plan)
+    first = [t.clone() for t in c.mxs_kv_read(small, pos, dtype=torch.float32)]
+    c.mxs_kv_write(x, x, small, pos, pos=pos, rope=plan, stream=torch.cuda.current_stream())
+    again = c.mxs_kv_read(small, pos, dtype=torch.float32, stream=torch.cuda.current_stream())
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    with pytest.raises(ValueError):
+        c.mxs_rope(x, pos.int(), plan)
+    with pytest.raises(ValueError):
+        c.mxs_rope(x, pos.cpu(), plan)
+    with pytest.raises(TypeError):
+        c.mxs_rope(x.half(), pos, plan)
+    with pytest.raises(ValueError):
+        c.mxs_kv_write(x, x, small, pos[:4])
+    with pytest.raises(ValueError):
+        c.mxs_kv_read(small, pos[None])
+    with pytest.raises(c.MxsError) as e:
+        c.mxs_rope(x, pos, c.mxs_rope_plan(256))
+    assert e.value.status == 2
+
+
+def test_a_workspace_of_exactly_the_size(c):
+    q, cache, batch, _, _ = _case(c, [5000, 700], [4, 60], 8, 2, 128, 4, 16, True, seed=19)
+    for dt in (torch.bfloat16, torch.float32):
+        need = c.mxs_attn_tree_workspace_bytes(q, cache, batch, dt)
+        assert need > 0
+        buf = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        first = -buf.data_ptr() % 256
+        want = c.mxs_attn_tree(q, cache, batch, 0.1, dtype=dt)
+        assert torch.equal(c.mxs_attn_tree(q, cache, batch, 0.1, dtype=dt, workspace=buf[first: first + need]), want)
+        assert torch.all(buf[:first] == 0xA5) and torch.all(buf[first + need:] == 0xA5)
+        with pytest.raises(c.MxsError) as e:
+            c.mxs_attn_tree(q, cache, batch, 0.1, dtype=dt, workspace=buf[first: first + need - 1])
+        assert e.value.status == 9
+
+
+def test_two_streams_at_once(c):
+    """Calls that overlap, each with memory of its own."""
+    cases = [_case(c, [1500, 300], [6, 9], 8, 2, 128, 4, 16, False, seed=20),
+             _case(c, [900], [70], 16, 2, 64, 8, 16, True, seed=21)]
+    want = [c.mxs_attn_tree(q, cache, batch, 0.1) for q, cache, batch, *_ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, (s, (q, cache, batch, *_)) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(s):
+                outs[i].append(c.mxs_attn_tree(q, cache, batch, 0.1))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for os, w in zip(outs, want) for o in os)
 
 
 def test_workspace_refusals(c):
