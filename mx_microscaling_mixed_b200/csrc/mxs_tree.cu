@@ -129,16 +129,6 @@ __device__ __forceinline__ bool any_of256(int half, bool p) {
 __device__ __forceinline__ void half_sync(int half) {
   asm volatile("barrier.cta.sync %0, 256;" ::"r"(half + 1) : "memory");
 }
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -168,37 +158,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// bf16 bits of 2^(b - 129), the step of a 4-bit block with scale byte b.
-__device__ __forceinline__ uint32_t step4(uint32_t b) { return b >= 3u ? (b - 2u) << 7 : 1u << (b + 4u); }
-// ... and 2^(b - 133), that of an 8-bit block.
-__device__ __forceinline__ uint32_t step8(uint32_t b) { return b >= 7u ? (b - 6u) << 7 : 1u << b; }
-
-// 8 codes -> 8 exact bf16 values.  4 bits (one word): the nibble with its
-// sign bit flipped in the mantissa of 128.0 is 136 + q, and
-// fma(136 + q, s, -136 s) = q s.  8 bits (two words), q = 16 h + l:
-// fma(136 + h, 16 s, -2304 s) = (16 h - 128) s, then fma(128 + l, s, .) = q s;
-// every intermediate is exact in bf16.  Two codes per instruction come from
-// the two halves of a word, so the values leave in the order 0 4 1 5 2 6 3 7
-// (4 bits) or 0 2 1 3 of each word (8 bits); q and the output follow it.
 // The factors of a block by its scale byte come from a table in shared
 // memory (a dozen instructions per block otherwise).
-template <int M>
-struct BlockScale {
-  uint32_t s, c, s16;
-};
-template <>
-struct BlockScale<4> {
-  uint32_t s, c;
-};
 template <int M>
 constexpr int kTableEntry = M == 4 ? 8 : 16;
 template <int M, int THREADS>
 __device__ __forceinline__ void fill_table(uint8_t *table) {
   for (uint32_t i = threadIdx.x; i < 256; i += THREADS) {
-    const uint32_t b = min(i, 249u);             // above, -136 s leaves bf16's range
-    const uint32_t c = (0x8000u | ((b + 5u) << 7) | (M == 4 ? 8u : 16u)) * 0x10001u;
-    if constexpr (M == 4) *reinterpret_cast<uint2 *>(table + 8 * i) = make_uint2(step4(b) * 0x10001u, c);
-    else *reinterpret_cast<uint4 *>(table + 16 * i) = make_uint4(step8(b) * 0x10001u, c, step4(b) * 0x10001u, 0);
+    const BlockScale<M> k = scale_factors<M>(min(i, kTopScale));
+    if constexpr (M == 4) *reinterpret_cast<uint2 *>(table + 8 * i) = make_uint2(k.s, k.c);
+    else *reinterpret_cast<uint4 *>(table + 16 * i) = make_uint4(k.s, k.c, k.s16, 0);
   }
 }
 template <int M>
@@ -210,21 +179,6 @@ __device__ __forceinline__ BlockScale<M> block_scale(const uint8_t *table, uint3
     const uint4 t = *reinterpret_cast<const uint4 *>(table + 16 * b);
     return {t.x, t.y, t.z};
   }
-}
-template <int M>
-__device__ __forceinline__ uint4 decode8(uint32_t w0, uint32_t w1, const BlockScale<M> &k) {
-  uint32_t o[4];
-  if constexpr (M == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fma2(((w0 >> (4 * i)) & 0x000F000Fu) ^ 0x43084308u, k.s, k.c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = (i < 2 ? w0 : w1) >> (8 * (i & 1));
-      o[i] = fma2((w & 0x000F000Fu) | 0x43004300u, k.s, fma2(((w >> 4) & 0x000F000Fu) ^ 0x43084308u, k.s16, k.c));
-    }
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 // The same order for 8 values of q.
 template <int M>

@@ -197,6 +197,31 @@ def test_write_is_rope_then_quantize(c):
             assert torch.equal(got.scale_rows(2), want.scale_rows(2))
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_read_of_every_code_at_every_scale(c, bits):
+    """Values are code * 2^(scale byte - 127 - bits + 2), from the smallest
+    subnormals to overflow."""
+    n_slots, d = 256, 64 if bits == 4 else 256
+    cache = c.kv_cache_empty(n_slots, 1, d, bits)
+    seg = 2 if bits == 4 else 0
+    rng = np.random.default_rng(bits)
+    for t in (cache.K, cache.V):
+        codes = np.stack([rng.permutation(256).astype(np.uint8) for _ in range(n_slots)])[:, : d * bits // 8]
+        scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], d // 32, axis=1)
+        t.code_rows(seg).copy_(torch.from_numpy(codes).cuda())
+        t.scale_rows(seg).copy_(torch.from_numpy(scales).cuda())
+    out32 = c.mxs_kv_read(cache, torch.arange(n_slots, device="cuda"), dtype=torch.float32)
+    out16 = c.mxs_kv_read(cache, torch.arange(n_slots, device="cuda"))
+    for t, a, b in zip((cache.K, cache.V), out32, out16):
+        raw = t.code_rows(seg).cpu().numpy()
+        q = raw.view(np.int8).astype(np.float64) if bits == 8 else np.stack(
+            [((raw & 15) ^ 8).astype(np.float64) - 8, ((raw >> 4) ^ 8).astype(np.float64) - 8], axis=-1).reshape(n_slots, d)
+        with np.errstate(over="ignore"):
+            want = (q * 2.0 ** (np.arange(256)[:, None] - 127.0 - bits + 2)).astype(np.float32)
+        assert np.array_equal(a[:, 0].cpu().numpy(), want)
+        assert torch.equal(b[:, 0].cpu(), torch.from_numpy(want).bfloat16())
+
+
 def test_slots_out_of_range_are_skipped_and_recorded(c):
     cache = c.kv_cache_empty(6, 2, 64)
     k = _randn(4, 2, 64, seed=6, dtype=torch.bfloat16)
