@@ -39,15 +39,18 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeArgs a, const
   const int half = plan.rot >> 1;
   const bool inter = plan.layout == MXS_ROPE_INTERLEAVED;
   const int step = VEC ? 8 : 1;
-  const int group = !VEC ? 1 : inter ? 4 : 8;            // pairs of a unit
+  const int shift = !VEC ? 0 : inter ? 2 : 3, group = 1 << shift;    // pairs of a unit
   // units of a head: turned ones first, then copied ones
-  const int turned = (half + group - 1) / group;
+  const int turned = (half + group - 1) >> shift;
   const int first_copied = VEC && inter ? turned * 8 : plan.rot;
   const int per_head = turned + (a.d - first_copied) / step;
   const int per_token = per_head * a.heads;
   const int wide = min(per_token, kRopeThreads);
   const int abreast = kRopeThreads / wide;               // tokens that the CTA's threads take at once
-  const int sub = threadIdx.x / wide;
+  const int sub = threadIdx.x / wide, r0 = threadIdx.x - sub * wide;
+  const int t_first = threadIdx.x / half, p_first = threadIdx.x - t_first * half;
+  const int t_by = kRopeThreads / half, p_by = kRopeThreads - t_by * half;
+  const int h0 = r0 / per_head;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
@@ -55,8 +58,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeArgs a, const
     // evaluated, turned and copied units alike
     constexpr int B = FIN ? 2 : 4;
     Raw8<FIN> v[B], w[B];
-    auto fetch = [&](int r, int t) {
-      const int h = r / per_head, u = r - h * per_head;
+    auto fetch = [&](int h, int u, int t) {
       const int e = u < turned ? u * 8 : first_copied + (u - turned) * 8;
 #pragma unroll
       for (int b = 0; b < B; ++b) {
@@ -66,23 +68,28 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeArgs a, const
         if (tb < nt && u < turned && !inter) w[b] = fetch8<FIN>(a.x, xi + half);
       }
     };
-    const int r0 = threadIdx.x - sub * wide;
-    if (VEC && sub < abreast) fetch(r0, sub);
+    if (VEC && sub < abreast) fetch(h0, r0 - h0 * per_head, sub);
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-      const int t = i / half, p = i - t * half;
-      turn[(t * group + p % group) * turned + p / group] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], a.inverse);
+    for (int t = t_first, p = p_first; t < nt;) {
+      turn[(t * group + (p & (group - 1))) * turned + (p >> shift)] =
+          rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], a.inverse);
+      t += t_by;
+      p += p_by;
+      if (p >= half) {
+        p -= half;
+        ++t;
+      }
     }
     __syncthreads();
     if (sub >= abreast) continue;
     for (int r = r0; r < per_token; r += wide) {
-      const int h = r / per_head, u = r - h * per_head;
+      const int h = r == r0 ? h0 : r / per_head, u = r - h * per_head;
       const bool turns = u < turned;
       if constexpr (VEC) {
         const int e = turns ? u * 8 : first_copied + (u - turned) * 8;
         const bool two = turns && !inter;
         for (int t = sub; t < nt; t += B * abreast) {
-          if (r > r0 || t > sub) fetch(r, t);
+          if (r > r0 || t > sub) fetch(h, u, t);
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             const int tb = t + b * abreast;
