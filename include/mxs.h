@@ -460,8 +460,10 @@ mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const int64_t *slot
  *   them (or whose rows leave q, or with a negative length or count) is left
  *   out, a page outside the pool reads as keys and values of zero; both are
  *   recorded as MXS_ERR_SHAPE for mxs_sync.
- *   ws (device, 256-byte aligned): mxs_attn_tree_workspace_bytes, the
- *   splits' partial results; calls that may overlap need one each.
+ *   ws (device, 256-byte aligned): mxs_attn_tree_workspace_bytes,
+ *   partial results of what no CTA finishes alone (a size for the longest
+ *   batch that max_q and max_len allow; no initial contents); calls that may
+ *   overlap need one each.
  * Decoded cache values are exact (scale bytes above 249, values of 2^122 and
  * more, read as 249); scores and sums are fp32.  The weights enter the
  * product with V in 8 significant bits for a bf16 out, in 24 for fp32. */
