@@ -403,7 +403,8 @@ mxs_status mxs_rope(const void *x, mxs_dtype xt, int64_t T, int64_t heads, int64
 /* A K/V cache: a pool of n_slots token slots of n_kvh heads.  K and V are
  * quantised tensors of n_slots*n_kvh rows in the same identity layout of one
  * width, {0, 0, d} (4 bits) or {d, 0, 0} (8 bits); row slot*n_kvh + g is kv
- * head g of the token in that slot.  d: a multiple of 32, at most 256.
+ * head g of the token in that slot.  d: a multiple of 32, at most 256;
+ * n_slots < 2^31; n_kvh rows of codes (and of scales) below 2^32 bytes.
  * (A 4-bit cache of d = 128 is what mxs_attn_decode reads, tokens in slot
  * order.) */
 typedef struct {

@@ -47,27 +47,37 @@ __device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits) {
   r.sc = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
   return r;
 }
-// kRoundBits + the code of x
-template <int M>
-__device__ __forceinline__ uint32_t raw_code(float x, CodeScale s) {
-  constexpr uint32_t L = (1u << (M - 1)) - 1u;
-  const uint32_t b = __float_as_uint(fmaf(x * s.pre, s.sc, kRoundMagic));
-  return min(max(b, kRoundBits - L), kRoundBits + L);
-}
 template <int M>
 __device__ __forceinline__ uint32_t code_of(float x, CodeScale s) {
-  return raw_code<M>(x, s) & ((1u << M) - 1u);
+  constexpr uint32_t L = (1u << (M - 1)) - 1u;
+  const uint32_t b = __float_as_uint(fmaf(x * s.pre, s.sc, kRoundMagic));
+  return min(max(b, kRoundBits - L), kRoundBits + L) & ((1u << M) - 1u);
 }
-// A word of codes as a sum modulo 2^32 of code + 2^(M-1) in each field (one
-// multiply-add per value instead of a mask, a shift and an or); flipping the
-// fields' top bits makes two's complement of them.
+__device__ __forceinline__ uint32_t clamp2(uint32_t x, uint32_t lo, uint32_t hi) {
+  asm("max.s16x2 %0, %0, %1;\n\tmin.s16x2 %0, %0, %2;" : "+r"(x) : "r"(lo), "r"(hi));
+  return x;
+}
+// A word of codes from 32 / M values.  With 2^(M-1) more in the constant (an
+// even number: ties go the same way) the sums' low halves are code +
+// 2^(M-1), from 0 to 2^M; two of them are clamped at once, the fields added
+// up, and flipping their top bits makes two's complement of them.
 template <int M>
-__device__ __forceinline__ uint32_t code_word(const float *x, CodeScale s) {
-  constexpr uint32_t kOnes = M == 4 ? 0x11111111u : 0x01010101u, kHalf = 1u << (M - 1);
+__device__ __forceinline__ uint32_t code_word(const float *x, float sc) {
+  constexpr uint32_t kHalf = 1u << (M - 1), kTop = 2 * kHalf - 1;
+  constexpr float kMagic = kRoundMagic + kHalf;
+  constexpr int N = 16 / M;                      // pairs k, k + N
   uint32_t sum = 0;
 #pragma unroll
-  for (int k = 0; k < 32 / M; ++k) sum += raw_code<M>(x[k], s) * (1u << (M * k));
-  return (sum - (kRoundBits - kHalf) * kOnes) ^ (kHalf * kOnes);
+  for (int k = 0; k < N; ++k) {
+    const uint32_t lo = __float_as_uint(fmaf(x[k], sc, kMagic)), hi = __float_as_uint(fmaf(x[k + N], sc, kMagic));
+    sum += clamp2(prmt(lo, hi, 0x5410), 0x00010001u, kTop * 0x10001u) << (M * k);
+  }
+  return sum ^ (M == 4 ? 0x88888888u : 0x80808080u);
+}
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
 }
 
 }  // namespace
@@ -90,51 +100,63 @@ __global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a,
   const int half = a.rope ? plan.rot >> 1 : 0;
   const bool inter = plan.layout == MXS_ROPE_INTERLEAVED;
   const int d = a.c.d, nh = a.c.n_kvh;
-  const int group = !VEC ? 1 : inter ? 4 : 8, groups = (half + group - 1) / group;
+  const int shift = !VEC ? 0 : inter ? 2 : 3, group = 1 << shift, groups = (half + group - 1) >> shift;
+  const int t_first = half ? threadIdx.x / half : 0, p_first = threadIdx.x - t_first * half;
+  const int t_by = half ? kWriteThreads / half : 0, p_by = kWriteThreads - t_by * half;
+  // the first unit's values of B tokens are on their way while cos and sin
+  // are evaluated
+  constexpr int B = 2;
+  const int per_head = d / 16, per_token = 2 * nh * per_head;      // K units, then V units; a multiple of 8
+  const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
+  const int sub = threadIdx.x / wide, r0 = threadIdx.x - sub * wide;
+  Raw8<F32> fv[B], fw[B];
+  int64_t fs[B];
+  struct Unit {
+    int isv, turned, h, e0, e1;                      // (turned: of K, to be turned)
+  };
+  auto unit = [&](int r) {
+    Unit k;
+    k.isv = r >= nh * per_head;
+    const int rr = r - k.isv * nh * per_head;
+    k.h = rr / per_head;
+    const int u = rr - k.h * per_head;
+    // K in the half layout: the turned run, then the rest; else one run
+    const int split = !k.isv && a.rope && !inter ? plan.rot : 0;
+    const int run0 = u < split / 16 ? 0 : split;
+    k.turned = !k.isv && a.rope && (inter || run0 == 0);
+    k.e0 = run0 + 8 * (u - run0 / 16);
+    k.e1 = k.e0 + (u < split / 16 ? split : d - split) / 2;
+    return k;
+  };
+  Unit un = unit(r0);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
-    // the first unit's values of B tokens are on their way while cos and sin
-    // are evaluated
-    constexpr int B = 2;
-    const int per_head = d / 16, per_token = 2 * nh * per_head;    // K units, then V units; a multiple of 8
-    const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
-    const int sub = threadIdx.x / wide, r0 = threadIdx.x - sub * wide;
-    Raw8<F32> fv[B], fw[B];
-    int64_t fs[B];
-    struct Unit {
-      int isv, h, run0, e0, e1;
-    };
-    auto unit = [&](int r) {
-      Unit k;
-      k.isv = r >= nh * per_head;
-      const int rr = r - k.isv * nh * per_head;
-      k.h = rr / per_head;
-      const int u = rr - k.h * per_head;
-      // K in the half layout: the turned run, then the rest; else one run
-      const int split = !k.isv && a.rope && !inter ? plan.rot : 0;
-      k.run0 = u < split / 16 ? 0 : split;
-      k.e0 = k.run0 + 8 * (u - k.run0 / 16);
-      k.e1 = k.e0 + (u < split / 16 ? split : d - split) / 2;
-      return k;
-    };
-    auto fetch = [&](const Unit &k, int t) {
+    auto fetch = [&](int t) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const int tb = t + b * abreast;
         fs[b] = tb < nt ? a.slot[t0 + tb] : -1;
         if (tb < nt) {                               // (also of a token without a slot: it is there)
-          const int64_t si = (t0 + tb) * a.ldt[k.isv] + k.h * a.ldh[k.isv];
-          fv[b] = fetch8<F32>(a.src[k.isv], si + k.e0);
-          fw[b] = fetch8<F32>(a.src[k.isv], si + k.e1);
+          const int64_t si = (t0 + tb) * a.ldt[un.isv] + un.h * a.ldh[un.isv];
+          fv[b] = fetch8<F32>(a.src[un.isv], si + un.e0);
+          fw[b] = fetch8<F32>(a.src[un.isv], si + un.e1);
         }
       }
     };
-    if (VEC && sub < abreast) fetch(unit(r0), sub);
+    if (VEC && sub < abreast) fetch(sub);
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * half; i += kWriteThreads) {
-      const int t = i / half, p = i - t * half;
-      turn[(t * group + p % group) * groups + p / group] = rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], false);
+    if (half) {
+      for (int t = t_first, p = p_first; t < nt;) {
+        turn[(t * group + (p & (group - 1))) * groups + (p >> shift)] =
+            rope_turn(plan.step[p], plan.gain, a.pos[t0 + t], false);
+        t += t_by;
+        p += p_by;
+        if (p >= half) {
+          p -= half;
+          ++t;
+        }
+      }
     }
     if (threadIdx.x < nt && a.slot[t0 + threadIdx.x] >= a.c.n_slots) record_bad_index(a.status);
     __syncthreads();
@@ -142,61 +164,65 @@ __global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a,
       if (sub >= abreast) continue;
       const uint32_t four = 0xFu << (lane & ~3);         // the lanes of a block of 32 values
       for (int r = r0; r < per_token; r += wide) {
-        const auto [isv, h, run0, e0, e1] = unit(r);
+        if (r > r0) un = unit(r);
         for (int tt = sub; tt < nt; tt += B * abreast) {
-          if (r > r0 || tt > sub) fetch(unit(r), tt);
+          if (r > r0 || tt > sub) fetch(tt);
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          const int t = tt + b * abreast;
-          const int64_t slot = fs[b];
-          if (slot < 0 || slot >= a.c.n_slots) continue;              // all lanes of the block
-          float v[8], w[8];
-          widen8<F32>(fv[b], v);
-          widen8<F32>(fw[b], w);
-          if (!isv && a.rope) {
-            const double2 *cs = turn + t * group * groups;
-            if (!inter) {
-              if (run0 == 0) {
+          for (int b = 0; b < B; ++b) {
+            const int t = tt + b * abreast;
+            if (static_cast<uint64_t>(fs[b]) >= static_cast<uint64_t>(a.c.n_slots)) continue;   // all lanes of the block
+            const uint32_t slot = static_cast<uint32_t>(fs[b]);
+            float x[2][8];
+            widen8<F32>(fv[b], x[0]);
+            widen8<F32>(fw[b], x[1]);
+            if (un.turned) {
+              const double2 *cs = turn + t * group * groups;
+              if (!inter) {
+                cs += un.e0 / 8;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) rope_pair(v[k], w[k], cs[k * groups + e0 / 8]);
-              }
-            } else {
+                for (int k = 0; k < 8; ++k) rope_pair(x[0][k], x[1][k], cs[k * groups]);
+              } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (e0 / 2 + k < half) rope_pair(v[2 * k], v[2 * k + 1], cs[k * groups + e0 / 8]);
-                if (e1 / 2 + k < half) rope_pair(w[2 * k], w[2 * k + 1], cs[k * groups + e1 / 8]);
+                for (int k = 0; k < 4; ++k) {
+                  if (un.e0 / 2 + k < half) rope_pair(x[0][2 * k], x[0][2 * k + 1], cs[k * groups + un.e0 / 8]);
+                  if (un.e1 / 2 + k < half) rope_pair(x[1][2 * k], x[1][2 * k + 1], cs[k * groups + un.e1 / 8]);
+                }
               }
             }
-          }
-          float av = 0.f, aw = 0.f;
+            uint32_t m[2];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            av = fmaxf(av, fabsf(v[k]));
-            aw = fmaxf(aw, fabsf(w[k]));
-          }
-          uint32_t mv = __float_as_uint(av), mw = __float_as_uint(aw);
+            for (int side = 0; side < 2; ++side) {
+              float top = 0.f;
 #pragma unroll
-          for (int o = 1; o <= 2; o <<= 1) {
-            mv = max(mv, __shfl_xor_sync(four, mv, o));
-            mw = max(mw, __shfl_xor_sync(four, mw, o));
-          }
-          const int64_t row = slot * nh + h;
-          uint8_t *cd = a.c.codes[isv] + row * a.c.code_pitch[isv];
-          uint8_t *sd = a.c.scales[isv] + row * a.c.scale_pitch[isv];
-#pragma unroll
-          for (int side = 0; side < 2; ++side) {
-            const CodeScale s = code_scale<M>(side ? mw : mv);
-            const float(&x)[8] = side ? w : v;
-            const int e = side ? e1 : e0;
-            if constexpr (M == 4) {
-              *reinterpret_cast<uint32_t *>(cd + e / 2) = code_word<4>(&x[0], s);
-            } else {
-              *reinterpret_cast<uint2 *>(cd + e) = make_uint2(code_word<8>(&x[0], s), code_word<8>(&x[4], s));
+              for (int k = 0; k < 8; k += 2) top = max3_abs(top, x[side][k], x[side][k + 1]);
+              m[side] = __float_as_uint(top);
             }
-            if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+              m[0] = max(m[0], __shfl_xor_sync(four, m[0], o));
+              m[1] = max(m[1], __shfl_xor_sync(four, m[1], o));
+            }
+            uint8_t *cd = a.c.codes[un.isv] + un.h * a.c.code_pitch[un.isv] + static_cast<uint64_t>(slot) * a.c.code_slot[un.isv];
+            uint8_t *sd = a.c.scales[un.isv] + un.h * a.c.scale_pitch[un.isv] + static_cast<uint64_t>(slot) * a.c.scale_slot[un.isv];
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+              const CodeScale s = code_scale<M>(m[side]);
+              float(&y)[8] = x[side];
+              if (s.pre != 1.f) {                    // (rare: a block below 2^-121)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] *= s.pre;
+              }
+              const int e = side ? un.e1 : un.e0;
+              if constexpr (M == 4) {
+                *reinterpret_cast<uint32_t *>(cd + e / 2) = code_word<4>(&y[0], s.sc);
+              } else {
+                *reinterpret_cast<uint2 *>(cd + e) = make_uint2(code_word<8>(&y[0], s.sc), code_word<8>(&y[4], s.sc));
+              }
+              if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
+            }
           }
         }
-        }
+        if (r + wide >= per_token && r > r0) un = unit(r0);
       }
     } else {
       const int nb = d / kBlock, per_token = 2 * nh * nb;
@@ -264,7 +290,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(ReadArgs a) {
   for (int r = threadIdx.x - sub * wide; r < per_token; r += wide) {
     const int side = r / per_side, rr = r - side * per_side, sv = a.first + side;
     const int h = rr / per_head, e = 8 * (rr - h * per_head);
-    const uint8_t *cd = a.c.codes[sv] + e * M / 8, *sd = a.c.scales[sv] + e / kBlock;
+    const uint8_t *cd = a.c.codes[sv] + h * a.c.code_pitch[sv] + e * M / 8;
+    const uint8_t *sd = a.c.scales[sv] + h * a.c.scale_pitch[sv] + e / kBlock;
+    const uint32_t code_slot = a.c.code_slot[sv], scale_slot = a.c.scale_slot[sv];
+    constexpr int kSize = FOUT ? 4 : 2;
+    uint8_t *dst = static_cast<uint8_t *>(a.dst[sv]) + ((t_first + sub) * a.ldt[sv] + h * a.ldh[sv] + e) * kSize;
+    const int64_t dst_next = abreast * a.ldt[sv] * kSize, dst_step = t_step * a.ldt[sv] * kSize;
     int64_t next[B];
     auto slots = [&](int64_t t0) {
 #pragma unroll
@@ -274,37 +305,40 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(ReadArgs a) {
       }
     };
     slots(t_first);
-    for (int64_t t0 = t_first; t0 < a.T; t0 += t_step) {
-      int64_t row[B];
+    for (int64_t t0 = t_first; t0 < a.T; t0 += t_step, dst += dst_step) {
+      bool real[B];
       uint2 c[B];
       uint32_t b[B];
 #pragma unroll
       for (int k = 0; k < B; ++k) {
-        if (next[k] >= a.c.n_slots) record_bad_index(a.status);
-        row[k] = next[k] >= 0 && next[k] < a.c.n_slots ? next[k] * a.c.n_kvh + h : -1;
-      }
-      if (t0 + t_step < a.T) slots(t0 + t_step);
-#pragma unroll
-      for (int k = 0; k < B; ++k) {
+        real[k] = static_cast<uint64_t>(next[k]) < static_cast<uint64_t>(a.c.n_slots);
+        if (!real[k] && next[k] >= 0) record_bad_index(a.status);
+        const uint32_t slot = static_cast<uint32_t>(next[k]);
         c[k] = make_uint2(0, 0);
         b[k] = 0;
-        if (row[k] < 0) continue;
-        if constexpr (M == 4) c[k].x = *reinterpret_cast<const uint32_t *>(cd + row[k] * a.c.code_pitch[sv]);
-        else c[k] = *reinterpret_cast<const uint2 *>(cd + row[k] * a.c.code_pitch[sv]);
-        b[k] = sd[row[k] * a.c.scale_pitch[sv]];
+        if (!real[k]) continue;
+        const uint8_t *cp = cd + static_cast<uint64_t>(slot) * code_slot;
+        if constexpr (M == 4) c[k].x = *reinterpret_cast<const uint32_t *>(cp);
+        else c[k] = *reinterpret_cast<const uint2 *>(cp);
+        b[k] = sd[static_cast<uint64_t>(slot) * scale_slot];
       }
+      if (t0 + t_step < a.T) slots(t0 + t_step);
+      uint8_t *o = dst;
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        if (row[k] < 0) continue;
+      for (int k = 0; k < B; ++k, o += dst_next) {
+        if (!real[k]) continue;
         // 8 exact bf16 values (a fifth of the instructions of widening them one by one), put in order
-        uint4 w = decode8<M>(c[k].x, c[k].y, scale_factors<M>(min(b[k], kTopScale)));
+        const bool mid = mid_scale<M>(b[k]);
+        BlockScale<M> factors = mid_factors<M>(b[k]);
+        if (!mid) factors = scale_factors<M>(min(b[k], kTopScale));
+        uint4 w = decode8<M>(c[k].x, c[k].y, factors);
         if constexpr (M == 4)
           w = make_uint4(prmt(w.x, w.y, 0x5410), prmt(w.z, w.w, 0x5410), prmt(w.x, w.y, 0x7632), prmt(w.z, w.w, 0x7632));
         else
           w = make_uint4(prmt(w.x, w.y, 0x5410), prmt(w.x, w.y, 0x7632), prmt(w.z, w.w, 0x5410), prmt(w.z, w.w, 0x7632));
         float v[8];
         widen8<false>(Raw8<false>{w}, v);
-        if (b[k] > kTopScale) {
+        if (!mid && b[k] > kTopScale) {
           const float step = pow2f(static_cast<int>(b[k]) - 127 - M + 2);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -314,13 +348,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(ReadArgs a) {
           }
           w = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
         }
-        const int64_t o = (t0 + sub + k * abreast) * a.ldt[sv] + h * a.ldh[sv] + e;
         if constexpr (VEC) {
-          if constexpr (FOUT) store8<true>(a.dst[sv], o, v);
-          else *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst[sv]) + o) = w;
+          if constexpr (FOUT) store8<true>(o, 0, v);
+          else *reinterpret_cast<uint4 *>(o) = w;
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) store1<FOUT>(a.dst[sv], o + i, v[i]);
+          for (int i = 0; i < 8; ++i) store1<FOUT>(o, i, v[i]);
         }
       }
     }
@@ -342,7 +375,13 @@ mxs_status cache_view(const mxs_kv_cache *c, CacheView *v) {
     v->scales[i] = t[i]->scales[seg];
     v->code_pitch[i] = t[i]->code_pitch[seg];
     v->scale_pitch[i] = t[i]->scale_pitch[seg];
+    const __int128 cs = static_cast<__int128>(c->n_kvh) * t[i]->code_pitch[seg];
+    const __int128 ss = static_cast<__int128>(c->n_kvh) * t[i]->scale_pitch[seg];
+    if (cs > UINT32_MAX || ss > UINT32_MAX) return MXS_ERR_SHAPE;
+    v->code_slot[i] = static_cast<uint32_t>(cs);
+    v->scale_slot[i] = static_cast<uint32_t>(ss);
   }
+  if (c->K.rows / c->n_kvh > INT32_MAX) return MXS_ERR_SHAPE;
   v->n_slots = c->K.rows / c->n_kvh;
   v->n_kvh = static_cast<int32_t>(c->n_kvh);
   v->d = static_cast<int32_t>(d);

@@ -8,7 +8,8 @@ namespace mxs {
 struct CacheView {
   uint8_t *codes[2], *scales[2];          // K, V
   int64_t code_pitch[2], scale_pitch[2];
-  int64_t n_slots;
+  uint32_t code_slot[2], scale_slot[2];   // bytes from a slot to the next
+  int64_t n_slots;                        // < 2^31
   int32_t n_kvh, d, bits;
 };
 
@@ -57,6 +58,20 @@ __device__ __forceinline__ BlockScale<M> scale_factors(uint32_t b) {
   const uint32_t c = (0x8000u | ((b + 5u) << 7) | (M == 4 ? 8u : 16u)) * 0x10001u;
   if constexpr (M == 4) return {step4(b) * 0x10001u, c};
   else return {step8(b) * 0x10001u, c, step4(b) * 0x10001u};
+}
+// The same where both factors are normal bf16 values, linear in b: all
+// scale bytes but a few at either end.
+template <int M>
+__device__ __forceinline__ bool mid_scale(uint32_t b) {
+  constexpr uint32_t lo = M == 4 ? 3 : 7;
+  return b - lo <= kTopScale - lo;
+}
+template <int M>
+__device__ __forceinline__ BlockScale<M> mid_factors(uint32_t b) {
+  const uint32_t x = b * 0x00800080u;
+  constexpr uint32_t c = ((0x8000u | (M == 4 ? 8u : 16u)) + (5u << 7)) * 0x10001u;
+  if constexpr (M == 4) return {x - 0x01000100u, x + c};
+  else return {x - 0x03000300u, x + c, x - 0x01000100u};
 }
 template <int M>
 __device__ __forceinline__ uint4 decode8(uint32_t w0, uint32_t w1, const BlockScale<M> &k) {

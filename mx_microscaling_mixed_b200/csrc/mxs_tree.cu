@@ -1286,69 +1286,104 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
 }
 
 // Joins an item's partial results, weighted by 2^(lse_j - lse) in the order
-// of the CTAs.  Block (c, chunk of 8 columns) takes the item that CTA c found
-// begun by the CTA before it, if that was the item's first; one warp a column.
+// of the CTAs.  Block (c, chunk of 8 W columns) takes the item that CTA c found
+// begun by the CTA before it, if that was the item's first; a warp takes W
+// columns, whose loads are in flight together.
+template <int R>
+constexpr int kJoinColumns = R >= 256 ? 4 : R >= 64 ? 2 : 1;
 template <int D, int R, bool FOUT>
 __global__ void __launch_bounds__(256) tree_combine_kernel(TreeArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, W = kJoinColumns<R>;
   const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
   const Meta m = a.meta[c];
   if (c >= m.parts || m.tile == 0) return;
   const Stretch st(m.total, m.parts);
   const int begin = st.begin(c), before = begin - st.begin(c - 1);
   if (m.tile > before) return;                       // an earlier CTA began it
-  const int col = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int i = (m.rt * R + col) / a.rep, h = m.rt * R + col - i * a.rep;
-  if (i >= m.n) return;
+  const int col = (blockIdx.y * 8 + (threadIdx.x >> 5)) * W;
+  const int columns = min(W, m.n * a.rep - m.rt * R - col);
+  if (columns <= 0) return;
   // parts: CTA c - 1 (its first or its last item), then the first items of c, c + 1, ... up to the item's end
   const int n = st.cta_of(begin - m.tile + m.tiles - 1) - c + 2;
-  auto part_of = [&](int j) {
-    const int64_t slot = j == 0 ? (static_cast<int64_t>(c) - 1) * 2 + (m.tile < before) : (static_cast<int64_t>(c) + j - 1) * 2;
-    return slot * R + col;
-  };
-  float top = -INFINITY, near = -INFINITY;           // near: part `lane`'s
-  bool nan = false;
-  for (int j = lane; j < n; j += 32) {
-    const float l = a.part_lse[part_of(j)];
-    if (j < 32) near = l;
-    nan |= l != l;
-    top = fmaxf(top, l);
+  // (columns behind the last row: read, as the workspace has them, and not used)
+  const int64_t slot0 = ((static_cast<int64_t>(c) - 1) * 2 + (m.tile < before)) * R + col;
+  const int64_t slot1 = static_cast<int64_t>(c) * 2 * R + col - 2 * R;
+  auto part_of = [&](int j) { return j == 0 ? slot0 : slot1 + j * (2 * R); };
+  float top[W], near[W];                             // near: part `lane`'s
+  bool nan[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    top[w] = near[w] = -INFINITY;
+    nan[w] = false;
   }
-  nan = __any_sync(0xffffffffu, nan);
+  for (int j = lane; j < n; j += 32) {
+    const float *l = a.part_lse + part_of(j);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float total = 0.f, acc[E];
+    for (int w = 0; w < W; ++w) {
+      const float x = l[w];
+      if (j < 32) near[w] = x;
+      nan[w] |= x != x;
+      top[w] = fmaxf(top[w], x);
+    }
+  }
+  float total[W], acc[W][E];
 #pragma unroll
-  for (int k = 0; k < E; ++k) acc[k] = 0.f;
-  if (top != -INFINITY) {
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      if (j0 > 0) near = j0 + lane < n ? a.part_lse[part_of(j0 + lane)] : -INFINITY;
-      const float weight = exp2f(near - top);
-      const int m32 = min(32, n - j0);
-#pragma unroll 8
-      for (int j = 0; j < m32; ++j) {
-        const float *p = a.part + part_of(j0 + j) * D + lane * E;
-        const float w = __shfl_sync(0xffffffffu, weight, j);
-        float v[E];
-        if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
-        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
-        total += w;
+  for (int w = 0; w < W; ++w) {
+    nan[w] = __any_sync(0xffffffffu, nan[w]);
 #pragma unroll
-        for (int k = 0; k < E; ++k) acc[k] = fmaf(w, v[k], acc[k]);
+    for (int o = 16; o >= 1; o >>= 1) top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], o));
+    total[w] = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[w][k] = 0.f;
+  }
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    float weight[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (j0 > 0) near[w] = j0 + lane < n ? a.part_lse[part_of(j0 + lane) + w] : -INFINITY;
+      weight[w] = top[w] == -INFINITY ? 0.f : exp2f(near[w] - top[w]);
+    }
+    const int m32 = min(32, n - j0);
+#pragma unroll 8 / W
+    for (int j = 0; j < m32; ++j) {
+      const float *p = a.part + part_of(j0 + j) * D + lane * E;
+      float v[W][E];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if constexpr (E == 4) *reinterpret_cast<float4 *>(v[w]) = *reinterpret_cast<const float4 *>(p + w * D);
+        else *reinterpret_cast<float2 *>(v[w]) = *reinterpret_cast<const float2 *>(p + w * D);
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = __shfl_sync(0xffffffffu, weight[w], j);
+        total[w] += f;
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[w][k] = fmaf(f, v[w][k], acc[w][k]);
       }
     }
   }
-  const int64_t row = m.first + i, head = m.g * a.rep + h;
-  const float inv = nan ? NAN : total == 0.f ? 0.f : 1.f / total;
-  const int64_t at = row * a.ldot + head * a.ldoh + lane * E;
+  int i = (m.rt * R + col) / a.rep, h = m.rt * R + col - i * a.rep;
 #pragma unroll
-  for (int k = 0; k < E; ++k) {
-    if constexpr (FOUT) static_cast<float *>(a.out)[at + k] = acc[k] * inv;
-    else static_cast<__nv_bfloat16 *>(a.out)[at + k] = __float2bfloat16(acc[k] * inv);
+  for (int w = 0; w < W; ++w) {
+    if (w >= columns) break;
+    const int64_t row = m.first + i, head = m.g * a.rep + h;
+    const float inv = nan[w] ? NAN : total[w] == 0.f ? 0.f : 1.f / total[w];
+    const int64_t at = row * a.ldot + head * a.ldoh + lane * E;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const float y = total[w] == 0.f && !nan[w] ? 0.f : acc[w][k] * inv;
+      if constexpr (FOUT) static_cast<float *>(a.out)[at + k] = y;
+      else static_cast<__nv_bfloat16 *>(a.out)[at + k] = __float2bfloat16(y);
+    }
+    if (a.lse && lane == 0)
+      a.lse[row * a.n_qh + head] = nan[w] ? NAN : total[w] == 0.f ? -INFINITY : (top[w] + log2f(total[w])) * kLn2;
+    if (++h == a.rep) {
+      h = 0;
+      ++i;
+    }
   }
-  if (a.lse && lane == 0) a.lse[row * a.n_qh + head] = nan ? NAN : total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 namespace {
@@ -1430,7 +1465,7 @@ mxs_status launch_tree(const TreeArgs &a, cudaStream_t s) {
   launch_pdl(tree_kernel<D, M, R, P, FOUT>, dim3(static_cast<unsigned>(a.ctas)), dim3(S::kThreads), S::kBytes, s, a);
   count_launch();
   if (a.meta && a.ctas > 1) {
-    launch_pdl(tree_combine_kernel<D, R, FOUT>, dim3(static_cast<unsigned>(a.ctas - 1), R / 8), dim3(256), 0, s, a);
+    launch_pdl(tree_combine_kernel<D, R, FOUT>, dim3(static_cast<unsigned>(a.ctas - 1), R / (8 * kJoinColumns<R>)), dim3(256), 0, s, a);
     count_launch();
   }
   return cuda_status(cudaGetLastError());
@@ -1443,7 +1478,7 @@ mxs_status launch_rows(const TreeArgs &a, cudaStream_t s) {
   launch_pdl(tree_rows_kernel<D, M>, dim3(static_cast<unsigned>(a.ctas)), dim3(S::kThreads), S::kBytes, s, a);
   count_launch();
   if (a.meta && a.ctas > 1) {
-    launch_pdl(tree_combine_kernel<D, 256, false>, dim3(static_cast<unsigned>(a.ctas - 1), 256 / 8), dim3(256), 0, s, a);
+    launch_pdl(tree_combine_kernel<D, 256, false>, dim3(static_cast<unsigned>(a.ctas - 1), 256 / (8 * kJoinColumns<256>)), dim3(256), 0, s, a);
     count_launch();
   }
   return cuda_status(cudaGetLastError());
