@@ -53,8 +53,10 @@ __device__ __forceinline__ uint32_t code_of(float x, CodeScale s) {
   const uint32_t b = __float_as_uint(fmaf(x * s.pre, s.sc, kRoundMagic));
   return min(max(b, kRoundBits - L), kRoundBits + L) & ((1u << M) - 1u);
 }
+// Both halves to lo..hi.  As fp16 values these small integers are subnormal
+// and in the same order, and fp16 pairs have instructions for it.
 __device__ __forceinline__ uint32_t clamp2(uint32_t x, uint32_t lo, uint32_t hi) {
-  asm("max.s16x2 %0, %0, %1;\n\tmin.s16x2 %0, %0, %2;" : "+r"(x) : "r"(lo), "r"(hi));
+  asm("max.f16x2 %0, %0, %1;\n\tmin.f16x2 %0, %0, %2;" : "+r"(x) : "r"(lo), "r"(hi));
   return x;
 }
 // A word of codes from 32 / M values.  With 2^(M-1) more in the constant (an
@@ -105,27 +107,34 @@ __global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a,
   const int t_by = half ? kWriteThreads / half : 0, p_by = kWriteThreads - t_by * half;
   // the first unit's values of B tokens are on their way while cos and sin
   // are evaluated
-  constexpr int B = 2;
+  constexpr int B = 2, kSize = F32 ? 4 : 2;
   const int per_head = d / 16, per_token = 2 * nh * per_head;      // K units, then V units; a multiple of 8
   const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
-  const int sub = threadIdx.x / wide, r0 = threadIdx.x - sub * wide;
+  const int sub = threadIdx.x / wide;
+  int r0 = threadIdx.x - sub * wide;
+  // (each scheduler of an SM takes every fourth warp: with K first everywhere two of them would have all the turning)
+  if (wide <= kWriteThreads / 2 && threadIdx.x >= kWriteThreads / 2) r0 = r0 < wide / 2 ? r0 + wide / 2 : r0 - wide / 2;
   Raw8<F32> fv[B], fw[B];
   int64_t fs[B];
   struct Unit {
-    int isv, turned, h, e0, e1;                      // (turned: of K, to be turned)
+    int isv, turned, e0, e1;                         // (turned: of K, to be turned)
+    uint32_t code_at, scale_at;                      // from a slot's first byte to the head's
+    const uint8_t *src;                              // of token 0
   };
   auto unit = [&](int r) {
     Unit k;
     k.isv = r >= nh * per_head;
     const int rr = r - k.isv * nh * per_head;
-    k.h = rr / per_head;
-    const int u = rr - k.h * per_head;
+    const int h = rr / per_head, u = rr - h * per_head;
     // K in the half layout: the turned run, then the rest; else one run
     const int split = !k.isv && a.rope && !inter ? plan.rot : 0;
     const int run0 = u < split / 16 ? 0 : split;
     k.turned = !k.isv && a.rope && (inter || run0 == 0);
     k.e0 = run0 + 8 * (u - run0 / 16);
     k.e1 = k.e0 + (u < split / 16 ? split : d - split) / 2;
+    k.code_at = h * static_cast<uint32_t>(a.c.code_pitch[k.isv]);
+    k.scale_at = h * static_cast<uint32_t>(a.c.scale_pitch[k.isv]);
+    k.src = static_cast<const uint8_t *>(a.src[k.isv]) + h * a.ldh[k.isv] * kSize;
     return k;
   };
   Unit un = unit(r0);
@@ -138,9 +147,9 @@ __global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a,
         const int tb = t + b * abreast;
         fs[b] = tb < nt ? a.slot[t0 + tb] : -1;
         if (tb < nt) {                               // (also of a token without a slot: it is there)
-          const int64_t si = (t0 + tb) * a.ldt[un.isv] + un.h * a.ldh[un.isv];
-          fv[b] = fetch8<F32>(a.src[un.isv], si + un.e0);
-          fw[b] = fetch8<F32>(a.src[un.isv], si + un.e1);
+          const uint8_t *p = un.src + (t0 + tb) * a.ldt[un.isv] * kSize;
+          fv[b] = fetch8<F32>(p, un.e0);
+          fw[b] = fetch8<F32>(p, un.e1);
         }
       }
     };
@@ -202,23 +211,32 @@ __global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a,
               m[0] = max(m[0], __shfl_xor_sync(four, m[0], o));
               m[1] = max(m[1], __shfl_xor_sync(four, m[1], o));
             }
-            uint8_t *cd = a.c.codes[un.isv] + un.h * a.c.code_pitch[un.isv] + static_cast<uint64_t>(slot) * a.c.code_slot[un.isv];
-            uint8_t *sd = a.c.scales[un.isv] + un.h * a.c.scale_pitch[un.isv] + static_cast<uint64_t>(slot) * a.c.scale_slot[un.isv];
+            uint8_t *cd = a.c.codes[un.isv] + (static_cast<uint64_t>(slot) * a.c.code_slot[un.isv] + un.code_at);
+            uint8_t *sd = a.c.scales[un.isv] + (static_cast<uint64_t>(slot) * a.c.scale_slot[un.isv] + un.scale_at);
+            // the factors 2^(M-2-e), below 2^128 where the scale byte is M - 2 or more
+            float sc[2];
+#pragma unroll
+            for (int side = 0; side < 2; ++side)
+              sc[side] = __uint_as_float(((M - 2u + 254u) << 23) - (m[side] & 0x7F800000u));
+            if (__builtin_expect(min(m[0], m[1]) < ((M - 2u) << 23), 0)) {
+#pragma unroll
+              for (int side = 0; side < 2; ++side) {
+                const CodeScale s = code_scale<M>(m[side]);
+                sc[side] = s.sc;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[side][k] *= s.pre;
+              }
+            }
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
-              const CodeScale s = code_scale<M>(m[side]);
-              float(&y)[8] = x[side];
-              if (s.pre != 1.f) {                    // (rare: a block below 2^-121)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] *= s.pre;
-              }
               const int e = side ? un.e1 : un.e0;
               if constexpr (M == 4) {
-                *reinterpret_cast<uint32_t *>(cd + e / 2) = code_word<4>(&y[0], s.sc);
+                *reinterpret_cast<uint32_t *>(cd + e / 2) = code_word<4>(x[side], sc[side]);
               } else {
-                *reinterpret_cast<uint2 *>(cd + e) = make_uint2(code_word<8>(&y[0], s.sc), code_word<8>(&y[4], s.sc));
+                *reinterpret_cast<uint2 *>(cd + e) =
+                    make_uint2(code_word<8>(x[side], sc[side]), code_word<8>(x[side] + 4, sc[side]));
               }
-              if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(s.byte);
+              if ((lane & 3) == 0) sd[e / kBlock] = static_cast<uint8_t>(m[side] >> 23);
             }
           }
         }
@@ -442,7 +460,8 @@ extern "C" mxs_status mxs_kv_write(const void *k, int64_t ldkt, int64_t ldkh, co
   const int64_t abreast = std::max<int64_t>(1, std::min<int64_t>(16, kWriteThreads / per_token));
   a.tokens = static_cast<int32_t>(T >= 8 * abreast * sms ? 2 * abreast : T >= abreast * sms ? abreast : 1);
   const int64_t steps = (T + a.tokens - 1) / a.tokens;
-  const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 8));
+  // no more CTAs than run at once: a thread's place costs as much as coding 16 values
+  const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 3));
   const size_t smem = sizeof(double2) * a.tokens * ((half + 3) / 4 * 4);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const mxs_rope_plan &p = plan ? *plan : none;
