@@ -94,7 +94,7 @@ __device__ __forceinline__ float max3_abs(float m, float a, float b) {
 //   holds the k-th pairs of neighbouring units side by side, which leaves no
 //   bank conflict.  Otherwise one warp per block, one lane per position.
 template <bool F32, int M, bool VEC>
-__global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a, const __grid_constant__ mxs_rope_plan plan) {
+__global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(WriteArgs a, const __grid_constant__ mxs_rope_plan plan) {
   extern __shared__ double2 turn[];
   pdl_wait();
   pdl_trigger();
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(WriteArgs a,
   const int t_first = half ? threadIdx.x / half : 0, p_first = threadIdx.x - t_first * half;
   const int t_by = half ? kWriteThreads / half : 0, p_by = kWriteThreads - t_by * half;
   // the first unit's values of B tokens are on their way while cos and sin
-  // are evaluated
-  constexpr int B = 2, kSize = F32 ? 4 : 2;
+  // are evaluated (two tokens', at three CTAs per SM, took the same for bf16 and 11.0 against 9.1 us for fp32)
+  constexpr int B = 1, kSize = F32 ? 4 : 2;
   const int per_head = d / 16, per_token = 2 * nh * per_head;      // K units, then V units; a multiple of 8
   const int wide = min(per_token, kWriteThreads), abreast = kWriteThreads / wide;
   const int sub = threadIdx.x / wide;
@@ -461,7 +461,7 @@ extern "C" mxs_status mxs_kv_write(const void *k, int64_t ldkt, int64_t ldkh, co
   a.tokens = static_cast<int32_t>(T >= 8 * abreast * sms ? 2 * abreast : T >= abreast * sms ? abreast : 1);
   const int64_t steps = (T + a.tokens - 1) / a.tokens;
   // no more CTAs than run at once: a thread's place costs as much as coding 16 values
-  const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 3));
+  const int grid = static_cast<int>(std::min<int64_t>(steps, static_cast<int64_t>(sms) * 4));
   const size_t smem = sizeof(double2) * a.tokens * ((half + 3) / 4 * 4);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const mxs_rope_plan &p = plan ? *plan : none;

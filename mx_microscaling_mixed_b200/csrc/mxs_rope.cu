@@ -32,7 +32,7 @@ struct RopeArgs {
 // heads of 128, bf16, where the 134 MB of x and y need 20).  Otherwise a unit
 // is one pair or one copied value.
 template <bool FIN, bool FOUT, bool VEC>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeArgs a, const __grid_constant__ mxs_rope_plan plan) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a, const __grid_constant__ mxs_rope_plan plan) {
   extern __shared__ double2 turn[];
   pdl_wait();
   pdl_trigger();
@@ -55,8 +55,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeArgs a, const
        t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
     // a unit's values of B tokens are on their way while cos and sin are
-    // evaluated, turned and copied units alike
-    constexpr int B = FIN ? 2 : 4;
+    // evaluated, turned and copied units alike (twice as many, at three CTAs
+    // per SM, took 30.3 us where these take 28.3)
+    constexpr int B = FIN ? 1 : 2;
     Raw8<FIN> v[B], w[B];
     auto fetch = [&](int h, int u, int t) {
       const int e = u < turned ? u * 8 : first_copied + (u - turned) * 8;

@@ -1124,7 +1124,7 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
       if (t == 0) {
         // q of a new item, zero where there is no such row; negated for a negative scale
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-        constexpr int B = 4, kQ = R * D / 8 / (W * 32);
+        constexpr int B = 8, kQ = R * D / 8 / (W * 32);
 #pragma unroll 1
         for (int i0 = 0; i0 < kQ; i0 += B) {
           uint4 v[B];
@@ -1254,7 +1254,9 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
       if (has && whole && a.lse && !part) a.lse[row * a.n_qh + head] = lse2 * kLn2;
       if (has && !whole && !part) a.part_lse[slot] = lse2;
       uint16_t *out = static_cast<uint16_t *>(a.out) + row * a.ldot + head * a.ldoh + part * (D / 2);
-      float *left = a.part + slot * D + part * (D / 2);
+      // (unfinished: chunks of four positions, [chunk][row])
+      float4 *left = reinterpret_cast<float4 *>(a.part) +
+                     ((static_cast<int64_t>(blockIdx.x) * 2 + !first) * (D / 4) + part * (D / 8)) * R + q * 128 + tok;
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t o[16];
@@ -1268,8 +1270,10 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
             const float z = __uint_as_float(o[g8 + k]);
             y[true_position<M>(k)] = inv == 0.f ? 0.f : z * inv;
           }
-          if (!whole) store8<true>(left, c + g8, y);
-          else if (a.out_vec) store8<false>(out, c + g8, y);
+          if (!whole) {
+            left[(c + g8) / 4 * R] = make_float4(y[0], y[1], y[2], y[3]);
+            left[((c + g8) / 4 + 1) * R] = make_float4(y[4], y[5], y[6], y[7]);
+          } else if (a.out_vec) store8<false>(out, c + g8, y);
           else
 #pragma unroll
             for (int k = 0; k < 8; ++k) store1<false>(out, c + g8 + k, y[k]);
@@ -1290,7 +1294,7 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
 // begun by the CTA before it, if that was the item's first; a warp takes W
 // columns, whose loads are in flight together.
 template <int R>
-constexpr int kJoinColumns = R >= 256 ? 4 : R >= 64 ? 2 : 1;
+constexpr int kJoinColumns = R >= 64 ? 2 : 1;
 template <int D, int R, bool FOUT>
 __global__ void __launch_bounds__(256) tree_combine_kernel(TreeArgs a) {
   pdl_wait();
@@ -1386,6 +1390,70 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(TreeArgs a) {
   }
 }
 
+// The same behind tree_rows_kernel, whose partial outputs lie in chunks of
+// four positions, [chunk][row]: lane = row in the reads here as in the writes
+// there (row after row instead, 16 bytes of 32 rows per instruction, the
+// chunked prompt of 211 tokens took 73 us).  Block (c, 32 rows, 64
+// positions); a warp takes two chunks, four parts in flight.
+template <int D>
+__global__ void __launch_bounds__(256) tree_rows_combine_kernel(TreeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int R = 256, C = 2;
+  const int c = blockIdx.x + 1, warp = blockIdx.z * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const Meta m = a.meta[c];
+  if (c >= m.parts || m.tile == 0) return;
+  const Stretch st(m.total, m.parts);
+  const int begin = st.begin(c), before = begin - st.begin(c - 1);
+  if (m.tile > before) return;                       // an earlier CTA began it
+  const int row0 = blockIdx.y * 32, r = row0 + lane, rows = m.n * a.rep - m.rt * R;
+  if (row0 >= rows) return;
+  const int n = st.cta_of(begin - m.tile + m.tiles - 1) - c + 2;
+  auto slot_of = [&](int j) -> int64_t {
+    return j == 0 ? (static_cast<int64_t>(c) - 1) * 2 + (m.tile < before) : (static_cast<int64_t>(c) + j - 1) * 2;
+  };
+  // (rows behind the last: read, as the workspace has them, and not used)
+  float top = -INFINITY;
+  bool nan = false;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const float l = a.part_lse[slot_of(j) * R + r];
+    nan |= l != l;
+    top = fmaxf(top, l);
+  }
+  float total = 0.f, acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const int64_t slot = slot_of(j);
+    const float l = a.part_lse[slot * R + r], w = top == -INFINITY ? 0.f : exp2f(l - top);
+    const float4 *p = reinterpret_cast<const float4 *>(a.part) + (slot * (D / 4) + warp * C) * R + r;
+    total += w;
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const float4 v = p[k * R];
+      acc[4 * k] = fmaf(w, v.x, acc[4 * k]);
+      acc[4 * k + 1] = fmaf(w, v.y, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(w, v.z, acc[4 * k + 2]);
+      acc[4 * k + 3] = fmaf(w, v.w, acc[4 * k + 3]);
+    }
+  }
+  if (r >= rows) return;
+  const int i = (m.rt * R + r) / a.rep, h = m.rt * R + r - i * a.rep;
+  const int64_t row = m.first + i, head = m.g * a.rep + h;
+  const float inv = nan ? NAN : total == 0.f ? 0.f : 1.f / total;
+  uint16_t *out = static_cast<uint16_t *>(a.out) + row * a.ldot + head * a.ldoh + warp * 8;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = inv == 0.f ? 0.f : acc[k] * inv;
+  if (a.out_vec) store8<false>(out, 0, acc);
+  else
+#pragma unroll
+    for (int k = 0; k < 8; ++k) store1<false>(out, k, acc[k]);
+  if (a.lse && warp == 0)
+    a.lse[row * a.n_qh + head] = nan ? NAN : total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
 namespace {
 
 // Host checks that need no device; fills the shape part of *a.
@@ -1478,7 +1546,7 @@ mxs_status launch_rows(const TreeArgs &a, cudaStream_t s) {
   launch_pdl(tree_rows_kernel<D, M>, dim3(static_cast<unsigned>(a.ctas)), dim3(S::kThreads), S::kBytes, s, a);
   count_launch();
   if (a.meta && a.ctas > 1) {
-    launch_pdl(tree_combine_kernel<D, 256, false>, dim3(static_cast<unsigned>(a.ctas - 1), 256 / (8 * kJoinColumns<256>)), dim3(256), 0, s, a);
+    launch_pdl(tree_rows_combine_kernel<D>, dim3(static_cast<unsigned>(a.ctas - 1), 256 / 32, D / 64), dim3(256), 0, s, a);
     count_launch();
   }
   return cuda_status(cudaGetLastError());
