@@ -113,6 +113,10 @@ def test_cache_refusals(c):
         assert call(c, _cache(c, d=48)) == 2 and call(c, _cache(c, d=288)) == 2
         assert call(c, good, T=-1) == 1 and call(c, good, slot=None) == 1
         assert call(c, good, T=0, k=None, v=None, slot=None) == 0
+        assert call(c, _cache(c, rows=1 << 31, n_kvh=1)) == 2     # slots and a slot's bytes are 32-bit numbers
+        wide = _cache(c)
+        wide.K.scale_pitch[2] = 1 << 31
+        assert call(c, wide) == 2
         mis = _cache(c)
         mis.V.codes[2] += 8
         assert call(c, mis) == 3

@@ -137,6 +137,9 @@ def _quantized(x, bits):
     (7, 2, 96, 4, 96, "half", torch.float32),            # pairs across blocks of 32
     (4, 2, 256, 8, 192, "half", torch.bfloat16),
     (4, 1, 192, 4, 20, "interleaved", torch.bfloat16),
+    (1003, 5, 64, 8, 32, "interleaved", torch.float32),  # tokens that lie across the warps of a CTA
+    (1207, 3, 128, 4, 128, "half", torch.bfloat16),
+    (2501, 8, 128, 8, 128, "half", torch.bfloat16),
 ])
 def test_write_matches_oracle_and_read_returns_it(c, T, n_kvh, d, bits, rot, layout, dtype):
     n_slots = 2 * T + 3
@@ -220,6 +223,27 @@ def test_read_of_every_code_at_every_scale(c, bits):
             want = (q * 2.0 ** (np.arange(256)[:, None] - 127.0 - bits + 2)).astype(np.float32)
         assert np.array_equal(a[:, 0].cpu().numpy(), want)
         assert torch.equal(b[:, 0].cpu(), torch.from_numpy(want).bfloat16())
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_write_of_every_scale_and_every_tie(c, bits, dtype):
+    """Blocks whose maximum has each exponent that bf16 holds, with values at
+    the codes, half-way between two codes and beyond the largest code."""
+    d, top = 128, 2 ** (bits - 1)
+    e = np.arange(-126, 128)
+    steps = np.concatenate([np.arange(0, 2 * top) / 2.0, [top - 0.25]]) / (top / 2)     # in units of 2^e
+    steps = steps[:: max(1, len(steps) // 60)]
+    pat = np.resize(np.concatenate([steps, -steps]), d)
+    pat[::32] = 1.0                                                # the block's exponent is e or above
+    x = torch.from_numpy((pat * 2.0 ** e[:, None].astype(np.float64)).astype(np.float32)).cuda().to(dtype)[:, None, :]
+    x = torch.cat([x, torch.zeros_like(x[:1])])
+    cache = c.kv_cache_empty(x.shape[0], 1, d, bits)
+    c.mxs_kv_write(x, -x, cache, torch.arange(x.shape[0], device="cuda"))
+    c.mxs_sync()
+    for (codes, scales), y in zip(_codes(cache), (x, -x)):
+        oc, os_ = _quantized(y.float().cpu().numpy(), bits)
+        assert np.array_equal(scales.cpu().numpy(), os_) and np.array_equal(codes.cpu().numpy(), oc)
 
 
 def test_slots_out_of_range_are_skipped_and_recorded(c):
@@ -468,6 +492,19 @@ def test_strides_streams_and_repeats(c):
     b = c.mxs_attn_tree(q, cache, batch, 0.1)
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,counts", [(torch.bfloat16, [40, 33]), (torch.bfloat16, [9, 2]), (torch.float32, [9, 2])])
+def test_outputs_in_unaligned_rows(c, d, dtype, counts):
+    """Whole and joined items alike, into rows that allow no wide stores: the
+    bits of dense rows, and nothing between them."""
+    q, cache, batch, _, _ = _case(c, [1900, 700], counts, 10, 2, d, 4, 16, False, seed=d)
+    want = c.mxs_attn_tree(q, cache, batch, 0.1, dtype=dtype)
+    room = torch.full((q.shape[0], 10, d + 3), 7.0, dtype=dtype, device="cuda")
+    c.mxs_attn_tree(q, cache, batch, 0.1, out=room[:, :, 1: d + 1])
+    assert torch.equal(room[:, :, 1: d + 1], want)
+    assert torch.all(room[:, :, 0] == 7.0) and torch.all(room[:, :, d + 1:] == 7.0)
 
 
 MORE = [
