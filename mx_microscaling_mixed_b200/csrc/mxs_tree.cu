@@ -997,7 +997,7 @@ struct RowsShape {
 // maximum that weights are relative to moves, by a vote of the half, when a
 // score passes it by more than kSlack.
 //   64-token trees over 2 contexts of up to 65536 (512 rows of 128, 4 bits):
-// 283 us, tensor pipe 0.45 and exponentials 0.46 busy; 235 GFLOP need 143.
+// 278 us, tensor pipe 0.45 and exponentials 0.46 busy; 235 GFLOP need 143.
 // Each half's chain of scores, weights and product holds it.
 template <int D, int M>
 __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel(TreeArgs a) {
