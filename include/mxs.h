@@ -469,8 +469,8 @@ mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const int64_t *slot
  * more, read as 249); scores and sums are fp32.  The weights enter the
  * product with V in 8 significant bits for a bf16 out, in 24 for fp32.  The
  * tensor core's fp32 sums round towards zero: for a bf16 out that adds up to
- * 2^-27 of the result per token that one CTA sums (2^-9, half a step of bf16,
- * at 2^18 of them); for fp32 it is cut off every 1024 tokens. */
+ * 2^-27 of the result per token that one CTA sums (2^-9 at 2^18 of them); for
+ * fp32 it is cut off every 1024 tokens. */
 typedef struct {
     int64_t B, rows, max_q, max_len;
     const int32_t *q_start, *length;
