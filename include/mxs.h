@@ -140,12 +140,14 @@ mxs_status mxs_sync(void *stream);
 
 /* Diagnostic: sets, on the current device, how many SM clock cycles a
  * pipeline wait of the prefill GEMM's tensor-core kernels (the mxs_gemm
- * calls whose workspace size is non-zero) may spin before the kernel gives up: it records MXS_ERR_TIMEOUT
+ * calls whose workspace size is non-zero), and the waits for one tile of
+ * mxs_attn_tree's, may spin before the kernel gives up: it records MXS_ERR_TIMEOUT
  * in the status word, stops issuing, lets the copies and MMAs it already
  * issued finish (waits bounded by the default limit), frees its tensor
  * memory and returns; its output is then unspecified.  cycles <= 0 restores
- * the default (4e9 cycles, about 2 s); larger values are clamped to it.
- * Synchronous; applies to GEMM launches made after it returns.  Lets a test
+ * the default (4e9 cycles, about 2 s, for the GEMM; 2e9 for mxs_attn_tree);
+ * larger values are clamped to it.
+ * Synchronous; applies to launches made after it returns.  Lets a test
  * make a wait run out without a fault.  Errors: MXS_ERR_CUDA. */
 mxs_status mxs_set_wait_limit(int64_t cycles);
 

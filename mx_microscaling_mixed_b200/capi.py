@@ -768,8 +768,9 @@ def mxs_sync(stream=None) -> None:
 
 
 def mxs_set_wait_limit(cycles: int) -> None:
-    """Diagnostic: the spin limit (SM cycles) of the prefill GEMM kernels'
-    pipeline waits on the current device; 0 restores the default."""
+    """Diagnostic: the spin limit (SM cycles) of the pipeline waits of the
+    prefill GEMM and mxs_attn_tree kernels on the current device; 0 restores
+    the default."""
     _check(_lib.mxs_set_wait_limit(int(cycles)), "mxs_set_wait_limit")
 
 

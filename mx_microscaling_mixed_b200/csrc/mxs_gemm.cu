@@ -1082,7 +1082,8 @@ extern "C" mxs_status mxs_sync(void *stream) {
 
 extern "C" mxs_status mxs_set_wait_limit(int64_t cycles) {
   const long long v = cycles <= 0 ? kWaitLimit : std::min<long long>(cycles, kWaitLimit);
-  return cudaMemcpyToSymbol(g_wait_limit, &v, sizeof(v)) == cudaSuccess ? MXS_OK : MXS_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_wait_limit, &v, sizeof(v)) != cudaSuccess || !set_tree_wait(cycles)) return MXS_ERR_CUDA;
+  return MXS_OK;
 }
 
 extern "C" mxs_status mxs_gemm_workspace_bytes(const mxs_mxtensor *A, const mxs_mxtensor *W, size_t *bytes) {

@@ -55,6 +55,10 @@ inline bool ensure_smem(Kernel k, int bytes) {
   return ensure_smem_impl(reinterpret_cast<const void *>(k), bytes);
 }
 
+// Limit of the waits of mxs_attn_tree's kernels on the current device (SM
+// cycles; <= 0: the default).
+bool set_tree_wait(long long cycles);
+
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialisation and calls pdl_trigger() at its
 // start, so the next kernel in the stream may be scheduled once every CTA

@@ -75,7 +75,10 @@ constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kPeriod = 8;                       // tiles
 constexpr int kAtom = kTile * 128;               // 64 bf16 values of each token of a tile
 constexpr float kSlack = 24.f;                   // weights are kept below 2^kSlack
-constexpr long long kTreeWait = 2000000000LL;    // cycles (about 1 s)
+constexpr int kTreeWait = 2000000000;            // cycles (about 1 s)
+// Limit of the matrix warp's waits, which stop all other roles
+// (mxs_set_wait_limit lowers it for a diagnostic run).
+__device__ int g_tree_wait = kTreeWait;
 
 // Waits for a barrier's phase; gives up when the limit ran out or another
 // role has given up.
@@ -94,6 +97,26 @@ __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volati
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *given_up, int *status) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   return wait_long(bar, parity, given_up, status);
+}
+// A suspended wait may outlast a short limit: the matrix warp looks behind
+// each tile at what its waits and the products issued after them took.
+// (At each of the warp's waits the look took 4 % of the wide form;
+// the limit read in the other roles' waits too, 3 % of 7-token trees.)
+__device__ __forceinline__ bool in_time(uint32_t &since, uint32_t limit, volatile int *given_up, int *status) {
+  const uint32_t now = clock(), took = now - since;
+  since = now;
+  if (took <= limit) return true;
+  *given_up = 1;
+  atomicExch(status, static_cast<int>(MXS_ERR_TIMEOUT));
+  return false;
+}
+// Leaves no product in flight, whichever role gave up and when (a softmax
+// warp may, on the last products, after all of them were issued): a last
+// commit covers all that the warp issued, and the tensor memory is freed
+// after this wait.
+__device__ __forceinline__ void drain(uint32_t leader, uint64_t *bar, int *status) {
+  ptx::mma_commit_by(leader, bar);
+  if (!ptx::mbar_wait_cycles(bar, 0, kTreeWait)) atomicExch(status, static_cast<int>(MXS_ERR_TIMEOUT));
 }
 // One arrival for a warp whose lanes have each made their writes visible:
 // arrivals of single lanes on one barrier go through one after the other.
@@ -667,13 +690,16 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
     };
     Walk w = start_walk(a, start, R);
     const int total = start[0];
+    const uint32_t limit = g_tree_wait;
+    uint32_t since = clock();
+    bool late = false;
     bool ok = total == 0 || scores(0);
     for (int n = 0; ok && w.left > 0; w.next(a, R)) {
       const int nt = w.count();
       for (int t = 0; t < nt && ok; ++t, ++n) {
         // (the scores of n + 1 go where those of n - 1 were: their weights have been waited for)
         if (n + 1 < total) ok = scores(n + 1);
-        ok = ok && wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
+        ok = ok && !late && wait_phase(v_full + n % SV, (n / SV) & 1, given_up, a.status) &&
              wait_phase(p_full + (n & 1), (n >> 1) & 1, given_up, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -686,13 +712,10 @@ __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(Tr
           ptx::mma_bf16_by(leader, ptx::uniform(tmem_o), vd + k * (2048 >> 4), pd + k * (32 * S::kPWidth >> 4), S::kIdescO,
                            k > 0 ? 1u : more);
         ptx::mma_commit_by(leader, o_done + (n & 1));
+        late = !in_time(since, limit, given_up, a.status);
       }
     }
-    if (!ok) {
-      // leave no product in flight: a last commit covers all that were issued
-      ptx::mma_commit_by(leader, drained);
-      ptx::mbar_wait_cycles(drained, 0, kTreeWait);
-    }
+    if (total > 0) drain(leader, drained, a.status);
     __syncwarp();
   } else if (warp >= S::kSoftWarps) {
     // ------------------------------------------------- fetching and decoding
@@ -1047,6 +1070,8 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
   if (warp == S::kMmaWarp) {
     // ------------------------------------------------------ matrix products
     const uint32_t leader = ptx::elect_one();
+    const uint32_t limit = g_tree_wait;
+    uint32_t since = clock();
     bool ok = true;
     auto await = [&](uint64_t *b, uint32_t parity) {
       ok = __all_sync(0xffffffffu, ok && wait_phase(b, parity, given_up, a.status));
@@ -1099,13 +1124,11 @@ __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel
             if (q == nq2 - 1) ptx::mma_commit_by(leader, k_free + (n + 1) % SK);
           }
         }
+        ok = __all_sync(0xffffffffu, ok && in_time(since, limit, given_up, a.status));
       }
       w = after;
     }
-    if (!ok) {
-      ptx::mma_commit_by(leader, drained);
-      ptx::mbar_wait_cycles(drained, 0, kTreeWait);
-    }
+    if (total > 0) drain(leader, drained, a.status);
     __syncwarp();
   } else if (warp >= S::kSoftWarps) {
     // ------------------------------------------------- fetching and decoding
@@ -1569,6 +1592,12 @@ mxs_status launch_shape(const TreeArgs &a, const Cut &c, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool set_tree_wait(long long cycles) {
+  const int v = static_cast<int>(cycles <= 0 ? kTreeWait : std::min<long long>(cycles, kTreeWait));
+  return cudaMemcpyToSymbol(g_tree_wait, &v, sizeof(v)) == cudaSuccess;
+}
+
 }  // namespace mxs
 
 using namespace mxs;
