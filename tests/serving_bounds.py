@@ -1,5 +1,5 @@
 """Exact attention values and error bounds for the tests of mxs_attn_tree over
-many tiles.
+many tiles, and the inputs of the two tests that a lower precision must fail.
 
 A score is an exact fp32 number here: queries are multiples of 1/2 below 32
 and keys multiples of 2^-8, so that every partial sum of products has fewer
@@ -109,3 +109,33 @@ def cut(ctx, counts, rep, n_kvh, R, causal, max_q, ctas):
         most = max(most, mine)
         turns += any(b and not a for a, b in zip(halves, halves[1:]))
     return run, max(parts), most, turns
+
+
+# ------------------------------------------- inputs that a lower precision fails
+def two_tokens(n, d, seed):
+    """Two tokens for each of n rows: one with the largest score and V = 0,
+    the other with a weight below 1 of many bits: out = w V / (1 + w), where
+    S = |out|, so that the error is that of w alone."""
+    rng = np.random.default_rng(seed)
+    q = np.zeros((n, d), dtype=np.float32)
+    q[:, 0] = np.arange(1, n + 1) % 64 * 0.5                       # exact in bf16
+    K = np.zeros((2, d), dtype=np.float32)
+    K[0, 0] = 1.0
+    V = np.zeros((2, d), dtype=np.float32)
+    V[1] = (rng.integers(64, 128, d) / 64.0) * np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    return q, K, V
+
+
+def long_sums(tokens, d, seed):
+    """Positive values of several magnitudes: sums that grow by every token,
+    whose rounding towards zero adds up.  Scores are integers from -3 to 0 in
+    base 2, so that weights are powers of two and their sum has few bits."""
+    rng = np.random.default_rng(seed)
+    K = np.zeros((tokens, d), dtype=np.float32)
+    K[:, 0] = -rng.integers(0, 4, tokens).astype(np.float32)
+    K[0, 0] = 0.0
+    V = (rng.integers(64, 128, (tokens, d)) / 128.0 * 2.0 ** -rng.integers(0, 4, (tokens, 1))).astype(np.float32)
+    return K, V
+
+
+LN2_SCALE = float(np.float32(LN2))                                  # scale2_of: 1

@@ -160,3 +160,52 @@ def test_short_items_in_turn(c, counts, n_qh, dtype):
     rng = np.random.default_rng(8)
     ctx = [int(n) for n in rng.integers(0, 700, len(counts))]
     _run(c, (ctx, counts, n_qh, 8, 128, 8, 5, True), dtype, 0.05, 500, 3)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rep", [4, 20, 64])                         # 16, 32 and 64 columns
+def test_weights_of_an_fp32_output_have_24_bits(c, rep, d, bits):
+    """Fails with weights of two bf16 pieces, as test_serving_bounds.py shows."""
+    sm, B = 0.0731, 50
+    q, K, V = sb.two_tokens(B * rep, d, 1)
+    cache = c.kv_cache_empty(2, 1, d, bits)
+    k, v = (torch.from_numpy(x).cuda()[:, None, :] for x in (K, V))
+    c.mxs_kv_write(k, v, cache, torch.arange(2, device="cuda"))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = c.tree_batch(torch.arange(B + 1, **i32), torch.ones(B, **i32), torch.zeros((B, 1), **i32), 2, max_q=1, max_len=2)
+    qt = torch.from_numpy(q).cuda().view(B, rep, d).to(torch.bfloat16)
+    out, lse = c.mxs_attn_tree(qt, cache, batch, sm, dtype=torch.float32, return_lse=True)
+    c.mxs_sync()
+    K, V = (x[:, 0].double() for x in c.mxs_kv_read(cache, torch.arange(2, device="cuda"), dtype=torch.float32))
+    e = sb.exact(qt.double().reshape(-1, d), K, V, sb.scale2_of(sm))
+    tol, tol_lse = sb.bounds(e, True, 1)
+    assert bool(((out.double().reshape(-1, d) - e["out"]).abs() <= tol).all())
+    assert bool(((lse.double().reshape(-1) - e["lse"] * math.log(2.0)).abs() <= tol_lse).all())
+
+
+@pytest.mark.parametrize("bits,d", [(8, 64), (8, 128), (4, 64)])
+@pytest.mark.parametrize("rep", [4, 20, 40])                         # 16, 32 and 64 columns
+def test_sums_of_an_fp32_output_start_again(c, rep, d, bits):
+    """256 tiles of an item in each CTA.  Fails with sums that stay in the
+    tensor core, as test_serving_bounds.py shows."""
+    tiles, B = 256, _sms()
+    n = tiles * sb.TILE
+    K, V = sb.long_sums(n, d, 2)
+    cache = c.kv_cache_empty(n, 1, d, bits)
+    k, v = (torch.from_numpy(x).cuda()[:, None, :] for x in (K, V))
+    c.mxs_kv_write(k, v, cache, torch.arange(n, device="cuda"))
+    q = torch.zeros((B, rep, d), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = torch.arange(rep, device="cuda") % 3
+    i32 = dict(dtype=torch.int32, device="cuda")
+    # (every sequence over the same pages: one item for each CTA)
+    batch = c.tree_batch(torch.arange(B + 1, **i32), torch.full((B,), n - 1, **i32), torch.zeros((B, 1), **i32), n, max_q=1,
+                         max_len=n)
+    wide = 2 if rep == 40 and d == 128 and bits == 8 else 1             # (32 columns there: two row tiles)
+    assert sb.cut([n - 1] * B, [1] * B, rep, 1, sb.columns(True, 1, rep, d, bits), True, 1, _sms())[:3] == (tiles, 1, wide)
+    out = c.mxs_attn_tree(q, cache, batch, sb.LN2_SCALE, dtype=torch.float32)
+    c.mxs_sync()
+    K, V = (x[:, 0].double() for x in c.mxs_kv_read(cache, torch.arange(n, device="cuda"), dtype=torch.float32))
+    e = sb.exact(q[0].double(), K, V, 1.0)
+    tol, _ = sb.bounds(e, True, tiles, exact_sums=True)
+    assert bool(((out.double() - e["out"]).abs() <= tol).all())
