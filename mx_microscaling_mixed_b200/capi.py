@@ -1,5 +1,6 @@
 """Binding of libmxs (the C ABI in include/mxs.h), same entry-point names: ctypes,
-and for the ordinary form of the serving calls a small extension module.
+and for the ordinary form of the serving calls a small extension module where
+one is built for the torch at hand (the general path gives the same results).
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  torch supplies device memory (inputs, outputs, workspaces) and
@@ -9,18 +10,34 @@ if it is missing this module raises on import -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass, field
 from typing import List, Optional, Sequence
 
 import torch
 
+from . import build as _build
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxs.so")
-for _path in (_LIB_PATH, os.path.join(os.path.dirname(_LIB_PATH), "_binding.so")):
-    if not os.path.exists(_path):
-        raise ImportError(f"{os.path.basename(_path)} not built at {_path}; run python -m mx_microscaling_mixed_b200.build")
+if not os.path.exists(_LIB_PATH):
+    raise ImportError(f"libmxs.so not built at {_LIB_PATH}; run python -m mx_microscaling_mixed_b200.build")
 _lib = ctypes.CDLL(_LIB_PATH)
-from . import _binding  # noqa: E402  (the serving calls' arguments in C++; linked against libmxs.so)
+
+
+def _load_binding():
+    """The extension that marshals the serving calls' arguments in C++ (linked
+    against libmxs.so), or None."""
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_binding = _load_binding()
 
 MXS_F32, MXS_BF16 = 0, 1
 MXS_ALLOC_FRACTIONS, MXS_ALLOC_BUDGET, MXS_ALLOC_LAYER = 0, 1, 2
@@ -508,7 +525,7 @@ def mxs_rope(x: torch.Tensor, pos: torch.Tensor, plan: RopePlan, *, inverse: boo
     """x (tokens, heads, d; bf16 or fp32) turned to its positions pos (int64),
     as `dtype` (x's by default); out may be x.  inverse turns back: the
     gradient of x from that of the result."""
-    if out is None and stream is None:
+    if _binding is not None and out is None and stream is None:
         r = _binding.rope(x, pos, plan.ptr, inverse, dtype)
         if r is not None:
             return _result(r, "mxs_rope")
@@ -559,7 +576,7 @@ def mxs_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slot: torch.T
     """Codes the tokens k, v (tokens, n_kvh, d) into their slots (int64; a
     negative one skips the token).  With `rope` the keys are turned to pos
     (int64) first."""
-    if stream is None:
+    if _binding is not None and stream is None:
         r = _binding.kv_write(k, v, cache.ptr, cache.index, slot, pos, None if rope is None else rope.ptr)
         if r is not None:
             return _check(r, "mxs_kv_write")
@@ -583,7 +600,7 @@ def mxs_kv_read(cache: KVCache, slot: torch.Tensor, *, dtype: torch.dtype = torc
     """(k, v), each (tokens, n_kvh, d): the values in the given slots (int64).
     A negative slot leaves its rows of `out` as they are (unspecified where
     the call makes them)."""
-    if out is None and stream is None:
+    if _binding is not None and out is None and stream is None:
         r = _binding.kv_read(cache.ptr, cache.index, slot, dtype)
         if r is not None:
             return _result(r, "mxs_kv_read")
@@ -683,7 +700,7 @@ def mxs_attn_tree(q: torch.Tensor, cache: KVCache, batch: TreeBatch, sm_scale: f
     are in `out` (unspecified where the call makes it)."""
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bf16")
-    if out is None and stream is None:
+    if _binding is not None and out is None and stream is None:
         r = _binding.attn_tree(q, cache.ptr, cache.index, batch.ptr, batch.index, sm_scale, dtype, return_lse, workspace)
         if r is not None:
             return _result(r, "mxs_attn_tree")
