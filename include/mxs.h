@@ -367,8 +367,11 @@ mxs_status mxs_layer_scores(const mxs_stack *m, const float *x, int64_t T, int64
  *                      rot ln(orig_len / (2 pi n)) / (2 ln theta); cos and
  *                      sin times 0.1 ln(factor) + 1.
  *   A frequency is kept as a fraction of a turn in 64-bit fixed point, so
- *   the phase of position p is the 64-bit product p * step modulo one turn:
- *   the angle is off by at most |p| * 2^-65 turns, for any int64 position.
+ *   the phase of position p is the 64-bit product p * step modulo one turn,
+ *   for any int64 position.  The step is off by its rounding, 2^-65 turns,
+ *   and by its evaluation in long double, some f_i (ln theta + 8) 2^-66
+ *   turns; |p| times that is the phase's error, and its rounding to a double
+ *   adds at most 2^-55 turns.
  *   rot even, 2..256; theta > 1; factor >= 1; 0 < low < high and orig_len
  *   >= 1 where they are used.  Errors: MXS_ERR_ARG. */
 enum { MXS_ROPE_HALF = 0, MXS_ROPE_INTERLEAVED = 1 };
@@ -467,12 +470,14 @@ mxs_status mxs_kv_read(const mxs_kv_cache *cache, int64_t T, const int64_t *slot
  *   partial results of what no CTA finishes alone (a size for the longest
  *   batch that max_q and max_len allow; no initial contents); calls that may
  *   overlap need one each.
- * Decoded cache values are exact (scale bytes above 249, values of 2^122 and
- * more, read as 249); scores and sums are fp32.  The weights enter the
- * product with V in 8 significant bits for a bf16 out, in 24 for fp32.  The
- * tensor core's fp32 sums round towards zero: for a bf16 out that adds up to
- * 2^-27 of the result per token that one CTA sums (2^-9 at 2^18 of them); for
- * fp32 it is cut off every 1024 tokens. */
+ * Decoded cache values are exact (scale bytes above 249, blocks whose largest
+ * magnitude is 2^123 or more, read as if they were 249); scores and sums are
+ * fp32.  The weights enter the product with V in 8 significant bits for a
+ * bf16 out, in 24 for fp32.  The tensor core's fp32 sums round towards zero:
+ * for a bf16 out that adds up to 2^-27 of sum_p softmax(s)_p |V[p][g]| for
+ * each token that one CTA sums (2^-9 of it at 2^18 tokens; where values of
+ * both signs cancel, more than that of the result); for fp32 it is cut off
+ * every 1024 tokens.  out must not overlap q. */
 typedef struct {
     int64_t B, rows, max_q, max_len;
     const int32_t *q_start, *length;

@@ -171,7 +171,7 @@ extern "C" mxs_status mxs_rope_plan_make(int32_t rot, int32_t layout, double the
   if (blend && (!(scaling->low > 0.0) || !(scaling->high > scaling->low) || !std::isfinite(scaling->high) ||
                 scaling->orig_len < 1))
     return MXS_ERR_ARG;
-  // long double throughout: the step is exact to the 64 bits it is kept in
+  // long double throughout (a relative error of a few 2^-64), then one rounding to 2^-64 turns
   const long double two_pi = 6.283185307179586476925286766559005768L;
   const long double th = theta, factor = blend || kind == MXS_ROPE_LINEAR ? scaling->factor : 1.0;
   long double a = 0, b = 0;
