@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a, const
     const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - t0));
     // a unit's values of B tokens are on their way while cos and sin are
     // evaluated, turned and copied units alike (twice as many, at three CTAs
-    // per SM, took 30.3 us where these take 28.3)
+    // per SM, took 30.3 us where these take 29.3)
     constexpr int B = FIN ? 1 : 2;
     Raw8<FIN> v[B], w[B];
     auto fetch = [&](int h, int u, int t) {

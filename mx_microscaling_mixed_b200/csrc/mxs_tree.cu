@@ -223,7 +223,7 @@ __device__ __forceinline__ int true_position(int e) {
 template <int D, int M, int R, int P>
 struct Shape {
   static constexpr int kSoftWarps = 8;                       // two groups of four
-  // For each of K and V.  (7-token trees over 32 contexts of up to 8191 tokens of 8 bits: 141 us with four, 178 with eight.)
+  // For each of K and V.  (Eight took a quarter longer: 7-token trees over 32 contexts of up to 8191 tokens of 8 bits.)
   static constexpr int kFetchWarps = 4;
   static constexpr int kMmaWarp = kSoftWarps + 2 * kFetchWarps;
   static constexpr int kThreads = (kMmaWarp + 1) * 32;
@@ -605,8 +605,8 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 // decoded once for all of them:
 //   S^T [token][row] = K Q^T     A = K  (token x d, K-major),  B = Q
 //   O^T [d][row]    += V^T P^T   A = V  (token x d, stored along d), B = P
-// Both accumulate in tensor memory.  Sixteen or eight warps fetch (asynchronous
-// copies, tiles ahead) and decode the cache into shared memory, half K and
+// Both accumulate in tensor memory.  Eight warps fetch (asynchronous copies,
+// a tile or two ahead) and decode the cache into shared memory, half K and
 // half V; one warp issues the products; eight warps turn scores into weights, four
 // for each half of the columns.  A softmax thread owns one token and sums its
 // weights per row over all tiles; the sums meet at an item's end.
@@ -618,11 +618,20 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 //   The tensor core's fp32 sums are rounded towards zero at every step: an
 // fp32 output is taken out of tensor memory every kPeriod tiles and summed
 // outside it (7-token trees over 8191 tokens: 3.5e-6 of the exact result
-// without that, 0.9e-6 with it).
+// without that, 0.9e-6 with it).  A bf16 output stays there: the error is
+// small next to the output's own rounding up to some 2^18 tokens of one CTA.
+//   Weights enter the product with V as P bf16 pieces: one for a bf16 output,
+// each weight off by up to 2^-8 of itself, which adds as much as the output's
+// rounding does (2.3e-3 of the result in all, 1.7e-3 with fp32 weights);
+// three for an fp32 output, 24 bits.  With three, trees of 16 take 43.6 us
+// where one takes 36.7, and the products of the wide form would triple; a
+// caller who needs the difference asks for fp32.
 //   Trees of up to 16 tokens over 8 contexts of up to 4096 (64 rows of 128,
-// 4 bits): 36 us, 10.4 tiles per SM; the cache's 29.6 MB need 4.5.  7-token
-// trees over 32 contexts of up to 8191 (21 rows of 64, 8 bits, fp32 output):
-// 145 us, issue slots 0.62 busy, DRAM 0.50; 211 MB need 32.
+// 4 bits): 36 us, of which 10.8 tiles per SM are 16 (2900 cycles each) and
+// finding the work, the first tile and joining the rest; the cache's 29.6 MB
+// need 4.5.  7-token trees over 32 contexts of up to 8191 (21 rows of 64,
+// 8 bits, fp32 output): 149 us, issue slots 0.62 busy, DRAM 0.50; 211 MB need
+// 32, and 583 are read.
 template <int D, int M, int R, int P, bool FOUT>
 __global__ void __launch_bounds__(Shape<D, M, R, P>::kThreads, 1) tree_kernel(TreeArgs a) {
   using S = Shape<D, M, R, P>;
@@ -1020,8 +1029,10 @@ struct RowsShape {
 // maximum that weights are relative to moves, by a vote of the half, when a
 // score passes it by more than kSlack.
 //   64-token trees over 2 contexts of up to 65536 (512 rows of 128, 4 bits):
-// 278 us, tensor pipe 0.45 and exponentials 0.46 busy; 235 GFLOP need 143.
-// Each half's chain of scores, weights and product holds it.
+// 287 us, tensor pipe 0.45 and exponentials 0.46 busy; 235 GFLOP need 143.
+// Each half's chain of scores, weights and product holds it.  Weights are one
+// bf16 piece (see tree_kernel): a second would fill the place of the scores
+// while half of them are still to be read, and run the output product twice.
 template <int D, int M>
 __global__ void __launch_bounds__(RowsShape<D, M>::kThreads, 1) tree_rows_kernel(TreeArgs a) {
   using S = RowsShape<D, M>;
